@@ -538,6 +538,107 @@ int pq2_linear_grouped(const void *x, int x_dtype, int64_t ldx, int64_t M,
                        int y_dtype, void *workspace, size_t workspace_bytes,
                        int32_t *dev_status, void *stream);
 
+/* Matrix-vector products with 4-bit weights and group scales: the output
+ * head (or any projection that ternary weights are too coarse for).
+ * Row n holds K codes of 4 bits, each G of them with an fp16 scale s and,
+ * with zero points, a zero point z in 0..15 (without them z = 8):
+ *   y[m][n] = sum_g s[n][g] * sum_{k in g} (c[n][k] - z[n][g]) * x[m][k]
+ * G = group = 128, 64 or 32;  K >= G a multiple of G (not of 128).
+ *
+ * pq2_w4_prepare — lays the weights out once in the order the kernel streams
+ * them.  A move of bits: values are unchanged.  It is an ordering point (see
+ * pq2_mmv_ex).
+ *   codes    (device) u8, N rows of K/2 bytes, ldc bytes apart (>= K/2);
+ *            column 2j is the low half of byte j, column 2j + 1 the high.
+ *   scales   (device) fp16 [N][K/G].
+ *   zeros    (device, NULL = no zero points) u8 [N][K/G]; only the low four
+ *            bits are read.
+ *   plane    (device) pq2_w4_plane_bytes(N, K, group, zeros != NULL) bytes,
+ *            16-byte aligned.
+ * pq2_w4_plane_bytes returns 0 for invalid arguments. */
+size_t pq2_w4_plane_bytes(int64_t N, int64_t K, int group, int zeros);
+int pq2_w4_prepare(const uint8_t *codes, int64_t ldc, const uint16_t *scales,
+                   const uint8_t *zeros, int64_t N, int64_t K, int group,
+                   uint8_t *plane, void *stream);
+
+/* pq2_w4_mmv — y = x W^T for M = 1..32.  The products are exact (c - z is a
+ * small integer, x a 16-bit value; a 32-bit x is taken as the sum of three
+ * bf16 parts, 24 bits in all), the group sums and y are fp32.
+ *   x        (device, or pinned host memory as for pq2_mmv) x_dtype
+ *            [M][ldx], ldx >= K; PQ2_BF16, PQ2_F16 or PQ2_F32 (|x| within
+ *            bf16's range).
+ *   zeros    non-zero if the plane was prepared with zero points.
+ *   plane    (device) from pq2_w4_prepare with the same N, K, group, zeros.
+ *   y        (device) y_dtype [M][N]; PQ2_F32, PQ2_BF16 or PQ2_F16, the fp32
+ *            result rounded to nearest even.
+ *   flags    PQ2_MMV_OVERLAP_WEIGHTS, PQ2_MMV_INDEPENDENT as for pq2_mmv_ex
+ *            (plane in the place of codes and scales); the kernel releases
+ *            the next one as soon as it starts.
+ * Column m is bit-identical for every M that contains it: the order of its
+ * additions depends on (N, K, group) and the device's SM count only. */
+int pq2_w4_mmv(const void *x, int x_dtype, int64_t ldx, int64_t M, int64_t N,
+               int64_t K, int group, int zeros, const uint8_t *plane, void *y,
+               int y_dtype, int flags, void *stream);
+
+/* Most alternatives per row that pq2_token_logprobs returns. */
+#define PQ2_MAX_TOP 32
+
+/* pq2_token_logprobs — per row of logits x, with t = scale * x and
+ * log p = t - log sum exp t:
+ *   token_logprobs[m][j] = log p[tokens[m][j]]
+ *   entropy[m]           = -sum p log p
+ *   top_ids[m][0..k)     = the k largest logits, descending, equal ones by
+ *                          the lower index;  top_logprobs their log p.
+ * A logit of -inf is excluded (p = 0).  A row that has only those: every log
+ * p is -inf, the entropy 0, top_ids 0..k-1.  A NaN or +inf in a row makes its
+ * log p and entropy NaN; in the order of the alternatives NaN is last.
+ *   logits   (device) dtype [M][ldl], ldl >= V; PQ2_BF16, PQ2_F16, PQ2_F32.
+ *   M        1 .. 1<<20;  V 1 .. 1<<30.
+ *   scale    1 / temperature, 0 < scale <= 1e6.
+ *   tokens   (device) int64 [M][T], T >= 0 (may be NULL when T = 0).  A
+ *            negative id marks no token (log p 0), an id >= V gives NaN.
+ *   token_logprobs (device) fp32 [M][T].
+ *   entropy  (device, may be NULL) fp32 [M].
+ *   k        0 .. min(V, PQ2_MAX_TOP).
+ *   top_ids, top_logprobs (device; may be NULL when k = 0) int64 and fp32
+ *            [M][k].
+ * Sums in fp32 in a fixed order: the same call gives the same bits.  Runs
+ * after the kernel before it on the stream and releases the next one as soon
+ * as it starts. */
+int pq2_token_logprobs(const void *logits, int dtype, int64_t ldl, int64_t M,
+                       int64_t V, float scale, const int64_t *tokens,
+                       int64_t T, float *token_logprobs, float *entropy,
+                       int k, int64_t *top_ids, float *top_logprobs,
+                       void *stream);
+
+/* pq2_norm_gate_residual — the RMS norms after a block and before the next
+ * one, fused with the block's gate and residual scale, per row of K columns:
+ *   p  = z / sqrt(mean z^2 + eps) * (w_post + w_offset)   (p = z if w_post
+ *        is NULL)
+ *   h' = h + alpha * gate * p         (no gate if NULL; h' = h if z is NULL)
+ *   n  = h' / sqrt(mean h'^2 + eps) * (w_pre + w_offset)
+ * in fp32 with IEEE square roots and divisions; h' is rounded for h_out only.
+ *   z, h     (device) dtype [M][ldz], [M][ldh], both strides >= K; z NULL
+ *            gives the plain norm of h (then no w_post, gate or h_out).
+ *   w_post, w_pre (device) dtype [K]; w_pre may be NULL if n_out is.
+ *   gate     (device, may be NULL) dtype, row m uses row m / rows_per_gate,
+ *            ldg >= K apart: rows_per_gate 1 is a gate per token, M one for
+ *            all, S one per sequence of S tokens.
+ *   w_offset added to both weights (1 for weights stored about 0).
+ *   eps      0 <= eps <= 1.
+ *   M        1 .. 1<<20;  K 1 .. PQ2_PREP_MAX_K.
+ *   h_out, n_out (device, one of them may be NULL) dtype [M][K].  h_out may
+ *            be h (when ldh = K); no other buffers may overlap.
+ * A missing operand of a part that is asked for is PQ2_ERR_NULL.  Runs after
+ * the kernel before it and releases the next one as soon as it starts. */
+int pq2_norm_gate_residual(const void *z, int64_t ldz, const void *h,
+                           int64_t ldh, int dtype, const void *w_post,
+                           const void *gate, int64_t ldg,
+                           int64_t rows_per_gate, float alpha,
+                           const void *w_pre, float w_offset, float eps,
+                           int64_t M, int64_t K, void *h_out, void *n_out,
+                           void *stream);
+
 /* Paths of pq2_debug_group_dots. */
 enum { PQ2_PATH_MMV_ADDXOR = 0, PQ2_PATH_MM = 1, PQ2_PATH_MMV_PLANES = 2,
        PQ2_PATH_MM_F8 = 3, PQ2_PATH_MMV_TC = 4 };

@@ -639,4 +639,91 @@ int pq2_mmv_geometry(int64_t N, int64_t K, int sm_count, int* ctas, int* threads
   return PQ2_OK;
 }
 
+namespace {
+
+bool valid_w4(int64_t N, int64_t K, int group) {
+  return (group == 128 || group == 64 || group == 32) && valid_n(N) && K >= group &&
+         K % group == 0 && K <= kMaxK;
+}
+bool valid_dtype(int t) { return t == PQ2_BF16 || t == PQ2_F16 || t == PQ2_F32; }
+bool valid_ld(int64_t ld, int64_t n) { return ld >= n && ld <= ((int64_t)1 << 40); }
+
+}  // namespace
+
+size_t pq2_w4_plane_bytes(int64_t N, int64_t K, int group, int zeros) {
+  if (!valid_w4(N, K, group)) return 0;
+  return pq2::w4_plane_bytes(N, K, group, zeros != 0);
+}
+
+int pq2_w4_prepare(const uint8_t* codes, int64_t ldc, const uint16_t* scales,
+                   const uint8_t* zeros, int64_t N, int64_t K, int group, uint8_t* plane,
+                   void* stream) {
+  if (!codes || !scales || !plane) return PQ2_ERR_NULL;
+  if (!valid_w4(N, K, group) || !valid_ld(ldc, K / 2)) return PQ2_ERR_SHAPE;
+  if (!aligned(scales, 2) || !aligned(plane, 16)) return PQ2_ERR_ALIGN;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return pq2::launch_w4_prepare(codes, ldc, scales, zeros, N, K, group, plane,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int pq2_w4_mmv(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t N, int64_t K,
+               int group, int zeros, const uint8_t* plane, void* y, int y_dtype, int flags,
+               void* stream) {
+  if (!x || !plane || !y) return PQ2_ERR_NULL;
+  if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype)) return PQ2_ERR_DTYPE;
+  if (flags & ~(PQ2_MMV_OVERLAP_WEIGHTS | PQ2_MMV_INDEPENDENT)) return PQ2_ERR_DTYPE;
+  if (M < 1 || M > 32 || !valid_w4(N, K, group) || !valid_ld(ldx, K)) return PQ2_ERR_SHAPE;
+  if (!aligned(x, elem_bytes(x_dtype)) || !aligned(plane, 16) || !aligned(y, elem_bytes(y_dtype)))
+    return PQ2_ERR_ALIGN;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  const int overlap = (flags & PQ2_MMV_INDEPENDENT) ? 2 : (flags & PQ2_MMV_OVERLAP_WEIGHTS) ? 1 : 0;
+  return pq2::launch_w4_mmv(x, x_dtype, ldx, M, N, K, group, zeros != 0, plane, y, y_dtype,
+                            overlap, sms, static_cast<cudaStream_t>(stream));
+}
+
+int pq2_token_logprobs(const void* logits, int dtype, int64_t ldl, int64_t M, int64_t V,
+                       float scale, const int64_t* tokens, int64_t T, float* token_logprobs,
+                       float* entropy, int k, int64_t* top_ids, float* top_logprobs,
+                       void* stream) {
+  if (!logits || (T > 0 && (!tokens || !token_logprobs)) || (k > 0 && (!top_ids || !top_logprobs)))
+    return PQ2_ERR_NULL;
+  if (!valid_dtype(dtype)) return PQ2_ERR_DTYPE;
+  if (M < 1 || M > kMaxM || !valid_n(V) || !valid_ld(ldl, V) || T < 0 || T > kMaxM || k < 0 ||
+      k > PQ2_MAX_TOP || k > V || !(scale > 0.f && scale <= 1e6f))
+    return PQ2_ERR_SHAPE;
+  if (!aligned(logits, elem_bytes(dtype)) || !aligned(tokens, 8) || !aligned(token_logprobs, 4) ||
+      !aligned(entropy, 4) || !aligned(top_ids, 8) || !aligned(top_logprobs, 4))
+    return PQ2_ERR_ALIGN;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  return pq2::launch_token_logprobs(logits, dtype, ldl, M, V, scale, tokens, T, token_logprobs,
+                                    entropy, k, top_ids, top_logprobs, sms,
+                                    static_cast<cudaStream_t>(stream));
+}
+
+int pq2_norm_gate_residual(const void* z, int64_t ldz, const void* h, int64_t ldh, int dtype,
+                           const void* w_post, const void* gate, int64_t ldg,
+                           int64_t rows_per_gate, float alpha, const void* w_pre,
+                           float w_offset, float eps, int64_t M, int64_t K, void* h_out,
+                           void* n_out, void* stream) {
+  if (!h || (!h_out && !n_out) || (n_out && !w_pre) || (!z && (w_post || gate || h_out)))
+    return PQ2_ERR_NULL;
+  if (!valid_dtype(dtype)) return PQ2_ERR_DTYPE;
+  if (M < 1 || M > kMaxM || K < 1 || K > PQ2_PREP_MAX_K || !valid_ld(ldh, K) ||
+      (z && !valid_ld(ldz, K)) || (gate && (!valid_ld(ldg, K) || rows_per_gate < 1)) ||
+      !(eps >= 0.f && eps <= 1.f) || (h_out == h && ldh != K))
+    return PQ2_ERR_SHAPE;
+  const int a = elem_bytes(dtype);
+  if (!aligned(z, a) || !aligned(h, a) || !aligned(w_post, a) || !aligned(gate, a) ||
+      !aligned(w_pre, a) || !aligned(h_out, a) || !aligned(n_out, a))
+    return PQ2_ERR_ALIGN;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  const pq2::NormParams p{z,   h,   w_pre, w_post, gate, h_out, n_out, ldz,
+                          ldh, ldg, rows_per_gate, M,    K,     alpha, eps, w_offset};
+  return pq2::launch_norm(p, dtype, sms, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -94,4 +94,28 @@ int launch_mm(const void* q_op, bool f8, const float* sx, const int32_t* qsum,
               int32_t* dots, int64_t M, int64_t N, int64_t K, int sm_count,
               int32_t* status, cudaStream_t stream, int act_group = 128);
 
+// 4-bit weights: raw row-major codes, scales and zero points -> the plane
+// pq2_w4_mmv streams; y = x W^T for M 1..32 (flags: PQ2_MMV_OVERLAP_WEIGHTS,
+// PQ2_MMV_INDEPENDENT as overlap 1 and 2 above).
+size_t w4_plane_bytes(int64_t N, int64_t K, int group, bool zeros);
+int launch_w4_prepare(const uint8_t* codes, int64_t ldc, const uint16_t* scales,
+                      const uint8_t* zeros, int64_t N, int64_t K, int group, uint8_t* plane,
+                      cudaStream_t stream);
+int launch_w4_mmv(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t N, int64_t K,
+                  int group, bool zeros, const uint8_t* plane, void* y, int y_dtype,
+                  int overlap, int sm_count, cudaStream_t stream);
+
+int launch_token_logprobs(const void* logits, int dtype, int64_t ldl, int64_t M, int64_t V,
+                          float scale, const int64_t* tokens, int64_t T, float* token_lp,
+                          float* entropy, int k, int64_t* top_ids, float* top_lp, int sm_count,
+                          cudaStream_t stream);
+
+struct NormParams {
+  const void *z, *h, *w_pre, *w_post, *gate;
+  void *h_out, *n_out;
+  int64_t ldz, ldh, ldg, rows_per_gate, M, K;
+  float alpha, eps, w_offset;
+};
+int launch_norm(const NormParams& p, int dtype, int sm_count, cudaStream_t stream);
+
 }  // namespace pq2

@@ -30,6 +30,8 @@ PQ2_PATH_MMV_ADDXOR, PQ2_PATH_MM, PQ2_PATH_MMV_PLANES, PQ2_PATH_MM_F8, PQ2_PATH_
     0, 1, 2, 3, 4
 PQ2_MMV_OVERLAP_WEIGHTS, PQ2_MMV_INDEPENDENT = 1, 2
 PQ2_STATIC_SCRATCH_BYTES = 1 << 20
+PQ2_MAX_TOP = 32
+PQ2_PREP_MAX_K = 32768
 GROUP = 128
 
 # C signatures, mirroring include/pq2.h.
@@ -69,6 +71,13 @@ SIGNATURES = {
     "pq2_linear_grouped_workspace_bytes": (_SZ, [_I64, _I64, _I]),
     "pq2_linear_grouped": (_I, [_P, _I, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _I, _P, _SZ, _P,
                                 _P]),
+    "pq2_w4_plane_bytes": (_SZ, [_I64, _I64, _I, _I]),
+    "pq2_w4_prepare": (_I, [_P, _I64, _P, _P, _I64, _I64, _I, _P, _P]),
+    "pq2_w4_mmv": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I, _I, _P, _P, _I, _I, _P]),
+    "pq2_token_logprobs": (_I, [_P, _I, _I64, _I64, _I64, ctypes.c_float, _P, _I64, _P, _P, _I,
+                                _P, _P, _P]),
+    "pq2_norm_gate_residual": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _I64, _I64, ctypes.c_float,
+                                    _P, ctypes.c_float, ctypes.c_float, _I64, _I64, _P, _P, _P]),
     "pq2_mmv_geometry": (_I, [_I64, _I64, _I, _P, _P, _P, _P]),
     "pq2_debug_mmv_drop_arrival": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P,
                                         _P]),
@@ -476,6 +485,95 @@ def pq2_linear_grouped(x, codes, scales, act_group: int, y=None, out_dtype=torch
         _ptr(y), _DT[y.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
         _ptr(status), _stream(stream)))
     return y
+
+
+def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stream=None):
+    """4-bit codes u8[N][K/2] (column 2j in the low half of byte j), fp16
+    scales [N][K/group] and zero points u8[N][K/group] (None: 8) -> the plane
+    u8 that pq2_w4_mmv streams."""
+    if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.stride(1) != 1:
+        raise ValueError("codes must be a 2-D uint8 tensor with unit column stride")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    for t, dt, what in ((scales, torch.float16, "fp16 scales"), (zeros, torch.uint8, "uint8 zeros")):
+        if t is not None and (t.dtype != dt or t.shape != (N, K // group)
+                              or not t.is_contiguous()):
+            raise ValueError(f"Expected contiguous {what} of shape [N][K / group]")
+    if plane is None:
+        nbytes = lib().pq2_w4_plane_bytes(N, K, group, int(zeros is not None))
+        plane = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=codes.device)
+    _check("pq2_w4_prepare", lib().pq2_w4_prepare(
+        _ptr(codes), codes.stride(0), _ptr(scales), _ptr(zeros), N, K, group, _ptr(plane),
+        _stream(stream)))
+    return plane
+
+
+def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
+               out_dtype=torch.float32, flags=0, stream=None):
+    """y[M][N] = x W^T for M = 1..32 on a plane of N rows from pq2_w4_prepare
+    (group and zeros as there)."""
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be 2-D with unit column stride")
+    M, K = x.shape
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    _check("pq2_w4_mmv", lib().pq2_w4_mmv(
+        _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, group, int(zeros), _ptr(plane), _ptr(y),
+        _DT[y.dtype], flags, _stream(stream)))
+    return y
+
+
+def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entropy: bool = True,
+                       out=None, stream=None):
+    """logits[M][V], tokens int64 [M][T] or [M] (None: none) ->
+    (token_logprobs [M][T], entropy [M] or None, top_ids int64 [M][k],
+    top_logprobs [M][k]); `out` is that tuple of buffers."""
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be 2-D with unit column stride")
+    M, V = logits.shape
+    if tokens is not None and (tokens.dtype != torch.int64 or not tokens.is_contiguous()
+                               or tokens.shape[0] != M):
+        raise ValueError("Expected contiguous int64 tokens with a row per row of logits")
+    T = 0 if tokens is None or not M else tokens.numel() // M
+    if out is None:
+        dev = logits.device
+        out = (torch.empty((M, T), dtype=torch.float32, device=dev),
+               torch.empty((M,), dtype=torch.float32, device=dev) if entropy else None,
+               torch.empty((M, k), dtype=torch.int64, device=dev),
+               torch.empty((M, k), dtype=torch.float32, device=dev))
+    _check("pq2_token_logprobs", lib().pq2_token_logprobs(
+        _ptr(logits), _DT[logits.dtype], logits.stride(0), M, V, scale, _ptr(tokens), T,
+        _ptr(out[0]) if T else None, _ptr(out[1]), k, _ptr(out[2]) if k else None,
+        _ptr(out[3]) if k else None, _stream(stream)))
+    return out
+
+
+def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: int = 1,
+                           alpha: float = 1.0, eps: float = 1e-6, w_offset: float = 0.0,
+                           h_out=None, n_out=None, stream=None):
+    """The norms around a block with its gate and residual scale:
+    h' = h + alpha * gate * norm(z, w_post), n = norm(h', w_pre) ->
+    (h_out, n_out).  z None: the plain norm of h (h_out None); w_pre None: no
+    n_out.  All tensors have h's type."""
+    for t in (z, h, gate):
+        if t is not None and (t.dim() != 2 or t.stride(1) != 1 or t.dtype != h.dtype):
+            raise ValueError("z, h and gate must be 2-D of one type with unit column stride")
+    M, K = h.shape
+    if z is not None and z.shape != h.shape:
+        raise ValueError("z and h must have one shape")
+    if gate is not None and (gate.shape[1] != K or gate.shape[0] * rows_per_gate < M):
+        raise ValueError("gate must have K columns and a row per rows_per_gate rows of h")
+    for t in (w_pre, w_post):
+        if t is not None and (t.shape != (K,) or t.dtype != h.dtype or not t.is_contiguous()):
+            raise ValueError("the norm weights must be contiguous [K] of h's type")
+    if h_out is None and z is not None:
+        h_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
+    if n_out is None and w_pre is not None:
+        n_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
+    _check("pq2_norm_gate_residual", lib().pq2_norm_gate_residual(
+        _ptr(z), 0 if z is None else z.stride(0), _ptr(h), h.stride(0), _DT[h.dtype],
+        _ptr(w_post), _ptr(gate), 0 if gate is None else gate.stride(0), rows_per_gate, alpha,
+        _ptr(w_pre), w_offset, eps, M, K, _ptr(h_out), _ptr(n_out), _stream(stream)))
+    return h_out, n_out
 
 
 def mmv_geometry(N: int, K: int, sm_count: int):
