@@ -561,12 +561,13 @@ int pq2_w4_prepare(const uint8_t *codes, int64_t ldc, const uint16_t *scales,
                    const uint8_t *zeros, int64_t N, int64_t K, int group,
                    uint8_t *plane, void *stream);
 
-/* pq2_w4_mmv — y = x W^T for M = 1..32.  The products are exact (c - z is a
- * small integer, x a 16-bit value; a 32-bit x is taken as the sum of three
- * bf16 parts, 24 bits in all), the group sums and y are fp32.
+/* pq2_w4_mmv — y = x W^T for M = 1..32.  c - z is exact, x is taken in fp16:
+ * an fp16 x as it is; a bf16 x scaled by a power of two per 128 columns
+ * (exact down to 2^-28 of the largest |x| among them, within 2^-39 of it
+ * below); a 32-bit x as the sum of two such parts (within 2^-24 of its
+ * value).  Products are exact, sums and y fp32.
  *   x        (device, or pinned host memory as for pq2_mmv) x_dtype
- *            [M][ldx], ldx >= K; PQ2_BF16, PQ2_F16 or PQ2_F32 (|x| within
- *            bf16's range).
+ *            [M][ldx], ldx >= K; PQ2_BF16, PQ2_F16 or PQ2_F32.
  *   zeros    non-zero if the plane was prepared with zero points.
  *   plane    (device) from pq2_w4_prepare with the same N, K, group, zeros.
  *   y        (device) y_dtype [M][N]; PQ2_F32, PQ2_BF16 or PQ2_F16, the fp32

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "pq2.h"
@@ -99,102 +100,176 @@ __global__ void w4_prepare_kernel(W4PrepParams p) {
 
 // ---------------------------------------------------------------------------
 // Product.
+//
+// A CTA holds a range of tiles and a range of units (all of them, or its
+// share when a cluster splits K).  It runs the units in passes of one unit
+// per warp: a warp keeps its unit's x in registers (the B fragments) and
+// streams that unit of tile after tile through a private ring of cp.async
+// copies, so a weight byte is read once and x once per CTA.  The warps' scaled
+// sums of a tile meet in shared memory, where they are added in unit order.
+// The order of a y's additions is therefore: MMA steps of a group, groups of
+// a unit, units of a CTA's range in ascending order, ranges in cluster order.
 
 struct W4Params {
   const void* x;
   const uint8_t* plane;
   void* y;
   int64_t ldx, N;
-  int M, K, units, y_dtype;
+  int M, K, y_dtype;
+  int tiles, units;     // of the matrix
+  int split;            // CTAs of a cluster, each with a share of the units
+  int block_tiles;      // tiles whose sums the accumulator holds
+  int batch_log;        // log2 of the tiles between two joins of the sums
+  int vector_x;         // x rows may be read 16 bytes at a time
+  int overlap;
 };
 
-// x as MMA columns: 16-bit types are taken as they are; a 32-bit x is the sum
-// of three bf16 parts (24 bits of mantissa), each a column of its own.
+// Operands are fp16 whatever x's type: a code OR-ed into the mantissa of 1024
+// is exactly 1024 + c (or 1024 + 16 c, four bits higher), and one fp16
+// operation makes it c - z, exactly.  (bf16 has 7 mantissa bits: the higher
+// field would need a shift of its own, 7 instead of 5 integer operations per
+// 8 weights, and integer operations run at half rate.)
+//
+// A bf16 or 32-bit x is scaled by a power of two, one per column and unit, so
+// that the unit's largest |x| lies in [2^14, 2^15).  A bf16 value is then
+// exact in fp16 down to 2^-28 of that largest one, and 2^-39 of it is the most
+// that rounding below costs.  A 32-bit x is the sum of two fp16 parts (within
+// 2^-24 of its value), each an MMA column of its own.
 template <typename XT>
-struct Operand {
-  using T = XT;
-  static constexpr int kParts = 1;
-};
-template <>
-struct Operand<float> {
-  using T = __nv_bfloat16;
-  static constexpr int kParts = 3;
-};
+constexpr int parts() {
+  return std::is_same<XT, float>::value ? 2 : 1;
+}
 
-template <typename T>
+__device__ __forceinline__ uint32_t bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+
+// d = a b + (first ? 0 : d)
+template <bool FIRST>
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T, __half>::value)
+  if constexpr (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The offset that turns a code into c - z in the operand type: a code OR-ed
-// into the mantissa of 128 (bf16) or 1024 (fp16) is exactly 128 + c or
-// 1024 + c, and subtracting 128 + z or 1024 + z is exact.
-template <typename T>
-struct Magic;
-template <>
-struct Magic<__nv_bfloat16> {
-  static constexpr uint32_t kBits = 0x43004300u;
-  static __device__ __forceinline__ uint32_t sub(uint32_t v, uint32_t off) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v),
-                                     *reinterpret_cast<__nv_bfloat162*>(&off));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
+// What turns the two fields of a row into c - z: 1024 + z to subtract from
+// the low one, 64 + z (negated) to add to a sixteenth of the high one.
+struct Offset {
+  __half2 low, high;
 };
-template <>
-struct Magic<__half> {
-  static constexpr uint32_t kBits = 0x64006400u;
-  static __device__ __forceinline__ uint32_t sub(uint32_t v, uint32_t off) {
-    const __half2 r =
-        __hsub2(*reinterpret_cast<__half2*>(&v), *reinterpret_cast<__half2*>(&off));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-};
-
-// The A fragment (rows i and i + 8) of one step's word.
-template <typename T>
-__device__ __forceinline__ void decode(uint32_t w, uint32_t off0, uint32_t off1, uint32_t* a) {
-  a[0] = Magic<T>::sub((w & 0x000F000Fu) | Magic<T>::kBits, off0);
-  a[1] = Magic<T>::sub(((w >> 4) & 0x000F000Fu) | Magic<T>::kBits, off1);
-  a[2] = Magic<T>::sub(((w >> 8) & 0x000F000Fu) | Magic<T>::kBits, off0);
-  a[3] = Magic<T>::sub(((w >> 12) & 0x000F000Fu) | Magic<T>::kBits, off1);
+__device__ __forceinline__ Offset offset_of(uint32_t z) {
+  return {half2_of((0x6400u + z) * 0x10001u), half2_of((0xD400u + 16 * z) * 0x10001u)};
 }
 
-// Part `part` of the 8 consecutive elements x[0..8) of one column as the two
-// B register pairs of two steps; zeros where the column does not exist.
+// (v & mask) | 0x64006400 in one operation.
+__device__ __forceinline__ __half2 field(uint32_t v, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(0x64006400u));
+  return half2_of(r);
+}
+
+// The A fragment of one step's word: row i is in the fields at bits 0 and 8,
+// row i + 8 in those at bits 4 and 12.
+__device__ __forceinline__ void decode(uint32_t w, __half2 low, __half2 high, uint32_t* a) {
+  const __half2 sixteenth = half2_of(0x2C002C00u);
+  const uint32_t v = w >> 8;
+  a[0] = bits(__hsub2(field(w, 0x000F000Fu), low));
+  a[1] = bits(__hfma2(field(w, 0x00F000F0u), sixteenth, high));
+  a[2] = bits(__hsub2(field(v, 0x000F000Fu), low));
+  a[3] = bits(__hfma2(field(v, 0x00F000F0u), sixteenth, high));
+}
+
+// 8 consecutive elements of x in fp32.
 template <typename XT>
-__device__ __forceinline__ uint4 load_b(const XT* x, int part, bool on) {
-  uint32_t r[4] = {};
-  if (on) {
+__device__ __forceinline__ void load8(const XT* x, bool vec, float* v) {
+  if constexpr (std::is_same<XT, float>::value) {
+    if (vec) {
+      const float4 lo = reinterpret_cast<const float4*>(x)[0];
+      const float4 hi = reinterpret_cast<const float4*>(x)[1];
+      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+      v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x[e];
+  } else {
+    uint32_t w[4];
+    if (vec) {
+      const uint4 q = *reinterpret_cast<const uint4*>(x);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = q[2 * e] | (uint32_t)q[2 * e + 1] << 16;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if constexpr (std::is_same<XT, float>::value) {
-        float v[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float f = x[2 * e + h];
-          for (int q = 0; q < part; ++q) f -= __bfloat162float(__float2bfloat16(f));
-          v[h] = f;
-        }
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
-        r[e] = *reinterpret_cast<const uint32_t*>(&b);
-      } else {
-        const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
-        r[e] = xb[2 * e] | (uint32_t)xb[2 * e + 1] << 16;
-      }
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The B fragments of column `part` of row x (null: zeros) over one unit, and
+// the factor that undoes their scaling.  Every lane of the warp calls it; the
+// four lanes of a column agree on the scaling.
+template <typename XT>
+__device__ __forceinline__ float load_b(const XT* x, int k, int K, int part, bool vec, uint4* b) {
+  if constexpr (std::is_same<XT, __half>::value) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      b[j] = make_uint4(0, 0, 0, 0);
+      if (x && k + 32 * j < K) {
+        if (vec) {
+          b[j] = *reinterpret_cast<const uint4*>(x + k + 32 * j);
+        } else {
+          const uint16_t* q = reinterpret_cast<const uint16_t*>(x + k + 32 * j);
+          b[j] = make_uint4(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16,
+                            q[4] | (uint32_t)q[5] << 16, q[6] | (uint32_t)q[7] << 16);
+        }
+      }
+    }
+    return 1.f;
+  } else {
+    float v[4][8];
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] = 0.f;
+      if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v[j]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[j][e]));
+    }
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    const int e8 = (int)(__float_as_uint(most) >> 23);
+    const int up = e8 == 255 ? 127 : min(268 - e8, 254);  // 2^(14 - exponent), as a biased exponent
+    const float scale = __uint_as_float((uint32_t)up << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float f0 = v[j][2 * e] * scale, f1 = v[j][2 * e + 1] * scale;
+        if (part) {
+          f0 -= __half2float(__float2half_rn(f0));
+          f1 -= __half2float(__float2half_rn(f1));
+        }
+        r[e] = bits(__floats2half2_rn(f0, f1));
+      }
+      b[j] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    return up == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - up) << 23);
+  }
 }
 
 __device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v) {
@@ -203,99 +278,359 @@ __device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v)
   else reinterpret_cast<__half*>(y)[at] = __float2half(v);
 }
 
-constexpr int kWarps = 8;
+constexpr int kPitch = 20;  // floats per column of 16 rows: conflict-free
 
-// One CTA per tile: its warps take the tile's units in turn, and their sums
-// are added through shared memory in warp order.
-template <typename XT, int NT, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(kWarps * 32) w4_mmv_kernel(W4Params p) {
-  using T = typename Operand<XT>::T;
-  constexpr int kParts = Operand<XT>::kParts;
-  constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
-  __shared__ float red[kWarps][kTileRows][8 * NT];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// Shape of a CTA by its MMA column tiles: warps (one unit each at a time),
+// CTAs an SM holds (registers and shared memory are bounded for that) and
+// ring stages.
+constexpr int kWarps = 8;
+template <int NT>
+struct Shape {
+  static constexpr int kPerSm = NT == 1 ? 3 : 2;
+  static constexpr int kStages = NT == 1 ? 5 : 4;
+  static constexpr int kSmem = (227 * 1024 - kPerSm * 1024) / kPerSm / 1024 * 1024;
+};
+
+// Shared memory by 32-bit address, and predicated without a branch: the loop
+// over tiles is bound by the instructions it issues.
+__device__ __forceinline__ void cp_async16_if(bool on, uint32_t dst, const void* src) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+      "l"(src), "r"((int)on)
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_if(bool on, uint32_t at, float v) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.shared.f32 [%0], %1;\n\t}" ::"r"(at),
+      "f"(v), "r"((int)on)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ void dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float acc[NT][4] = {};
-  for (int u = warp; u < p.units; u += kWarps) {
-    const uint8_t* unit =
-        p.plane + ((int64_t)blockIdx.x * p.units + u) * unit_bytes(GROUP, ZEROS);
-    const uint4 c0 = reinterpret_cast<const uint4*>(unit)[lane];
-    const uint4 c1 = reinterpret_cast<const uint4*>(unit + 512)[lane];
-    const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    uint4 b[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int v = 8 * nt + i, m = v / kParts;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = u * kUnitK + 32 * j + 8 * t;
-        const bool on = m < p.M && k < p.K;
-        b[nt][j] = load_b(static_cast<const XT*>(p.x) + (on ? m * p.ldx + k : 0), v % kParts, on);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const uint32_t sc = reinterpret_cast<const uint32_t*>(unit + kUnitCodeBytes)[8 * g + i];
-      const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sc));
-      uint32_t z0 = 8, z1 = 8;
-      if (ZEROS) {
-        const uint32_t z = unit[kUnitCodeBytes + 32 * kGroups + 8 * g + i];
-        z0 = z & 15, z1 = z >> 4;
-      }
-      const uint32_t off0 = Magic<T>::kBits + z0 * 0x10001u, off1 = Magic<T>::kBits + z1 * 0x10001u;
-      float d[NT][4] = {};
-#pragma unroll
-      for (int s2 = 0; s2 < kSteps; ++s2) {
-        const int step = g * kSteps + s2;
-        uint32_t a[4];
-        decode<T>(words[step], off0, off1, a);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 bb = b[nt][step / 2];
-          mma16816<T>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        acc[nt][0] = fmaf(s.x, d[nt][0], acc[nt][0]);
-        acc[nt][1] = fmaf(s.x, d[nt][1], acc[nt][1]);
-        acc[nt][2] = fmaf(s.y, d[nt][2], acc[nt][2]);
-        acc[nt][3] = fmaf(s.y, d[nt][3], acc[nt][3]);
-      }
-    }
-  }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    red[warp][i][8 * nt + 2 * t] = acc[nt][0];
-    red[warp][i][8 * nt + 2 * t + 1] = acc[nt][1];
-    red[warp][i + 8][8 * nt + 2 * t] = acc[nt][2];
-    red[warp][i + 8][8 * nt + 2 * t + 1] = acc[nt][3];
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < kTileRows * p.M; e += kWarps * 32) {
-    const int m = e / kTileRows, r = e % kTileRows;
-    const int64_t n = (int64_t)blockIdx.x * kTileRows + r;
-    if (n >= p.N) continue;
-    float sum = 0.f;
-    for (int q = kParts - 1; q >= 0; --q)  // the smallest part first
-      for (int w = 0; w < kWarps; ++w) sum += red[w][r][m * kParts + q];
-    store_y(p.y, p.y_dtype, (int64_t)m * p.N + n, sum);
-  }
 }
 
 template <typename XT, int NT, int GROUP, bool ZEROS>
-int launch_one(const W4Params& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(const W4Params p) {
+  constexpr int kParts = parts<XT>();
+  constexpr bool kScaled = !std::is_same<XT, __half>::value;
+  constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
+  constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
+  constexpr int kStages = Shape<NT>::kStages;
+  extern __shared__ __align__(16) uint8_t smem[];
+
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = lane >> 2, t = lane & 3;
+  const int cols = p.M * kParts;
+  uint8_t* const ring = smem + warp * (kStages * kUnitBytes);
+  float* const red = reinterpret_cast<float*>(smem + warps * (kStages * kUnitBytes));
+  const int red_warp = cols * kPitch, red_tile = warps * red_warp;
+  const int red_buf = red_tile << p.batch_log;
+  float* const acc = red + 2 * red_buf;
+
+  const int rank = blockIdx.x % p.split, cluster = blockIdx.x / p.split;
+  const int clusters = gridDim.x / p.split;
+  const int t0 = (int)((int64_t)cluster * p.tiles / clusters);
+  const int t1 = (int)((int64_t)(cluster + 1) * p.tiles / clusters);
+  const int u0 = (int)((int64_t)rank * p.units / p.split);
+  const int u1 = (int)((int64_t)(rank + 1) * p.units / p.split);
+  const int64_t tile_bytes = (int64_t)p.units * kUnitBytes;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!p.overlap) dependency_wait();
+
+  // The copies run kStages - 1 items ahead; items are (block of tiles, pass,
+  // tile), the last fastest.  `left`: tiles left of the pass being copied.
+  const uint32_t ring_end = smem_u32(ring) + kStages * kUnitBytes;
+  uint32_t dst = smem_u32(ring);
+  int lb = t0, left = min(p.block_tiles, t1 - t0), lu = u0 + warp;
+  bool go = lu < u1;
+  const uint8_t* src = p.plane + lb * tile_bytes + (int64_t)lu * kUnitBytes + lane * 16;
+  auto copy_next = [&](uint32_t slot) {
+    const uint32_t at = slot + lane * 16;
+    cp_async16_if(go, at, src);
+    cp_async16_if(go, at + 512, src + 512);
+    cp_async16_if(go && lane < kChunks - 64, at + 1024, src + 1024);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    src += tile_bytes;
+    if (--left == 0) {
+      lu += warps;
+      if (lu - warp >= u1) {
+        lu = u0 + warp;
+        lb += p.block_tiles;
+      }
+      left = min(p.block_tiles, t1 - lb);
+      go = lu < u1 && left > 0;
+      src = p.plane + lb * tile_bytes + (int64_t)lu * kUnitBytes + lane * 16;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    copy_next(dst);
+    dst += kUnitBytes;
+  }
+  if (p.overlap == 1) dependency_wait();
+
+  // dst: the slot that the item before the current one used; cur: its own.
+  uint32_t cur = smem_u32(ring);
+  bool on[NT][2];  // which of its MMA columns exist
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    on[nt][0] = 8 * nt + 2 * t < cols;
+    on[nt][1] = 8 * nt + 2 * t + 1 < cols;
+  }
+  const uint32_t out0 = smem_u32(red + warp * red_warp + 2 * t * kPitch + i);
+  uint4 b[NT][4];
+  float undo[NT][2];
+  int buf = 0;
+  bool waited = p.overlap != 2;
+  for (int b0 = t0; b0 < t1; b0 += p.block_tiles) {
+    const int b1 = min(b0 + p.block_tiles, t1);
+    for (int pu = u0; pu < u1 || pu == u0; pu += warps) {
+      const int u = pu + warp, active = min(warps, u1 - pu);
+      const bool last = pu + warps >= u1, idle = u >= u1;
+      if (!idle && (b0 == t0 || u1 - u0 > warps)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int v = 8 * nt + i, m = v / kParts;
+          const XT* x = m < p.M ? static_cast<const XT*>(p.x) + m * p.ldx : nullptr;
+          const float f = load_b(x, u * kUnitK + 8 * t, p.K, v % kParts, p.vector_x != 0, b[nt]);
+          if (kScaled) {
+            undo[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+            undo[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+          }
+        }
+      }
+      for (int tb = b0; tb < b1; tb += 1 << p.batch_log) {
+        const int te = min(tb + (1 << p.batch_log), b1);
+        uint32_t out = out0 + buf * red_buf * 4;
+        if (idle) {
+          for (int tile = tb; tile < te; ++tile) {
+            copy_next(dst);
+            dst = cur;
+            cur = cur + kUnitBytes == ring_end ? ring_end - kStages * kUnitBytes : cur + kUnitBytes;
+          }
+        } else {
+#pragma unroll 1
+          for (int tile = tb; tile < te; ++tile) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            copy_next(dst);
+            dst = cur;
+            const uint32_t codes = cur + lane * 16, side = cur + kUnitCodeBytes + i * 4;
+            cur += kUnitBytes;
+            cur = cur == ring_end ? ring_end - kStages * kUnitBytes : cur;
+            float sum[NT][4];
+            uint4 c;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const float2 s = __half22float2(half2_of(lds32(side + 32 * g)));
+              Offset o0, o1;
+              if (ZEROS) {
+                const uint32_t z = lds8(dst + kUnitCodeBytes + 32 * kGroups + 8 * g + i);
+                o0 = offset_of(z & 15), o1 = offset_of(z >> 4);
+              } else {
+                o0 = o1 = offset_of(8);
+              }
+              float d[NT][4];
+#pragma unroll
+              for (int s2 = 0; s2 < kSteps; ++s2) {
+                const int step = g * kSteps + s2;
+                if (step % 4 == 0) c = lds128(codes + step / 4 * 512);
+                const uint32_t w = step % 4 == 0 ? c.x : step % 4 == 1 ? c.y : step % 4 == 2 ? c.z : c.w;
+                uint32_t a[4];
+                decode(w, o0.low, o1.high, a);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint4 bb = b[nt][step / 2];
+                  if (s2 == 0)
+                    mma16816<true>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
+                  else
+                    mma16816<false>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
+                }
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float sc = e < 2 ? s.x : s.y;
+                  sum[nt][e] = g == 0 ? sc * d[nt][e] : fmaf(sc, d[nt][e], sum[nt][e]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t at = out + (8 * nt + h) * kPitch * 4;
+                sts_if(on[nt][h], at, kScaled ? sum[nt][h] * undo[nt][h] : sum[nt][h]);
+                sts_if(on[nt][h], at + 32, kScaled ? sum[nt][h + 2] * undo[nt][h] : sum[nt][h + 2]);
+              }
+            out += red_tile * 4;
+          }
+        }
+        __syncthreads();
+        // Join: one thread per (column, row of the batch), in unit order.
+        const bool done = last && p.split == 1 && kParts == 1;
+        if (done && !waited) {
+          dependency_wait();
+          waited = true;
+        }
+        const int rows_log = p.batch_log + 4, rows = (te - tb) * kTileRows;
+        for (int e = threadIdx.x; e < cols << rows_log; e += blockDim.x) {
+          const int v = e >> rows_log, r = e & ((1 << rows_log) - 1);
+          if (r >= rows) continue;
+          float* a = acc + (v * p.block_tiles + tb - b0) * kTileRows + r;
+          const float* q = red + buf * red_buf + (r >> 4) * red_tile + v * kPitch + (r & 15);
+          float sum = pu == u0 ? 0.f : *a;
+#pragma unroll 5
+          for (int w = 0; w < active; ++w) sum += q[w * red_warp];
+          if (done) {
+            const int64_t n = (int64_t)tb * kTileRows + r;
+            if (n < p.N) store_y(p.y, p.y_dtype, v * p.N + n, sum);
+          } else {
+            *a = sum;
+          }
+        }
+        buf ^= 1;
+      }
+    }
+    if (p.split == 1 && kParts == 1) continue;
+    if (!waited) {
+      dependency_wait();
+      waited = true;
+    }
+    // Parts of a 32-bit x (the smaller first) and ranges of the cluster.
+    if (p.split > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    const int rows = (b1 - b0) * kTileRows;
+    for (int e = threadIdx.x + rank * blockDim.x; e < rows * p.M; e += p.split * blockDim.x) {
+      const int m = e / rows, r = e % rows;
+      float y = 0.f;
+      for (int z = 0; z < p.split; ++z) {
+        float sum = 0.f;
+        for (int q = kParts - 1; q >= 0; --q) {
+          const float* a = acc + (m * kParts + q) * p.block_tiles * kTileRows + r;
+          float v;
+          if (p.split > 1)
+            asm volatile(
+                "{\n\t.reg .u32 at;\n\tmapa.shared::cluster.u32 at, %1, %2;\n\t"
+                "ld.shared::cluster.f32 %0, [at];\n\t}"
+                : "=f"(v)
+                : "r"(smem_u32(a)), "r"(z)
+                : "memory");
+          else
+            v = *a;
+          sum += v;
+        }
+        y += sum;
+      }
+      const int64_t n = (int64_t)b0 * kTileRows + r;
+      if (n < p.N) store_y(p.y, p.y_dtype, m * p.N + n, y);
+    }
+    if (p.split > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
+  if (!waited) dependency_wait();
+}
+
+// The split of K over a cluster orders the additions, so it depends on the
+// matrix and the SM count only.  A CTA's time is its passes times (its tiles +
+// the start of a pass, worth about 6 tiles), and a cluster's join is worth
+// about 4 more; taken where that is least, for three CTAs an SM.
+int w4_split(int tiles, int units, int sms) {
+  int split = 1;
+  int64_t least = INT64_MAX;
+  for (int c = 1; c <= 8 && c <= units; ++c) {
+    const int share = (units + c - 1) / c, passes = (share + kWarps - 1) / kWarps;
+    const int clusters = std::max(1, 3 * sms / c);
+    const int64_t cost = (int64_t)passes * ((tiles + clusters - 1) / clusters + 6) + (c > 1 ? 4 : 0);
+    if (cost < least) least = cost, split = c;
+  }
+  return split;
+}
+
+template <typename XT, int NT, int GROUP, bool ZEROS>
+int launch_one(W4Params p, int sms, cudaStream_t stream) {
+  using S = Shape<NT>;
+  auto kern = w4_mmv_kernel<XT, NT, GROUP, ZEROS>;
+  p.split = w4_split(p.tiles, p.units, sms);
+
+  // Clusters that fit the device at once, looked up once per device.
+  static std::atomic<int> resident[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PQ2_ERR_CUDA;
+  const int share = (p.units + p.split - 1) / p.split;
+  const int passes = (share + kWarps - 1) / kWarps;
+  const int warps = (share + passes - 1) / passes;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p.N + kTileRows - 1) / kTileRows));
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, w4_mmv_kernel<XT, NT, GROUP, ZEROS>, p) != cudaSuccess) {
+  int most = resident[dev][p.split].load(std::memory_order_acquire);
+  if (!most) {
+    cfg.gridDim = dim3(p.split);
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most < 1) {
+      cudaGetLastError();
+      return PQ2_ERR_CUDA;
+    }
+    resident[dev][p.split].store(most, std::memory_order_release);
+  }
+  // Equal shares: the clusters that run at once take as many tiles each.
+  const int each = (p.tiles + most - 1) / most;
+  const int clusters = (p.tiles + each - 1) / each;
+  const int cols = p.M * parts<XT>();
+  const int ring = warps * S::kStages * unit_bytes(GROUP, ZEROS);
+  const int red_tile = warps * cols * kPitch * 4, acc_tile = cols * kTileRows * 4;
+  const auto red = [&](int log) { return 2 * (red_tile << log); };
+  p.batch_log = 0;
+  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= 24 * 1024 &&
+         ring + red(p.batch_log + 1) + 4 * acc_tile <= S::kSmem)
+    ++p.batch_log;
+  p.block_tiles = std::min(each, (S::kSmem - ring - red(p.batch_log)) / acc_tile);
+  if (p.block_tiles < 1) return PQ2_ERR_SHAPE;
+
+  cfg.gridDim = dim3((unsigned)(clusters * p.split));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = ring + red(p.batch_log) + p.block_tiles * acc_tile;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
     cudaGetLastError();
     return PQ2_ERR_LAUNCH;
   }
@@ -303,28 +638,34 @@ int launch_one(const W4Params& p, cudaStream_t stream) {
 }
 
 template <typename XT, int NT>
-int launch_nt(const W4Params& p, int group, bool zeros, cudaStream_t stream) {
-  if (group == 128) return zeros ? launch_one<XT, NT, 128, true>(p, stream) : launch_one<XT, NT, 128, false>(p, stream);
-  if (group == 64) return zeros ? launch_one<XT, NT, 64, true>(p, stream) : launch_one<XT, NT, 64, false>(p, stream);
-  return zeros ? launch_one<XT, NT, 32, true>(p, stream) : launch_one<XT, NT, 32, false>(p, stream);
+int launch_nt(const W4Params& p, int group, bool zeros, int sms, cudaStream_t stream) {
+  switch (group * 2 + zeros) {
+    case 256: return launch_one<XT, NT, 128, false>(p, sms, stream);
+    case 257: return launch_one<XT, NT, 128, true>(p, sms, stream);
+    case 128: return launch_one<XT, NT, 64, false>(p, sms, stream);
+    case 129: return launch_one<XT, NT, 64, true>(p, sms, stream);
+    case 64: return launch_one<XT, NT, 32, false>(p, sms, stream);
+    default: return launch_one<XT, NT, 32, true>(p, sms, stream);
+  }
 }
 
 template <typename XT>
-int launch_x(W4Params p, int64_t M, int group, bool zeros, cudaStream_t stream) {
-  // At most 32 MMA columns at a time: 32 columns of x, or 10 of a 32-bit x.
-  constexpr int kMost = 32 / Operand<XT>::kParts;
+int launch_x(W4Params p, int64_t M, int group, bool zeros, int sms, cudaStream_t stream) {
+  // At most 32 MMA columns at a time: 32 columns of x, or 16 of a 32-bit x.
+  constexpr int kMost = 32 / parts<XT>();
   const int y_size = p.y_dtype == PQ2_F32 ? 4 : 2;
+  p.vector_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(XT) % 16 == 0;
   for (int64_t m = 0; m < M; m += kMost) {
     W4Params q = p;
     q.M = (int)std::min<int64_t>(kMost, M - m);
     q.x = static_cast<const XT*>(p.x) + m * p.ldx;
     q.y = static_cast<uint8_t*>(p.y) + m * p.N * y_size;
     int st;
-    switch ((q.M * Operand<XT>::kParts + 7) / 8) {
-      case 1: st = launch_nt<XT, 1>(q, group, zeros, stream); break;
-      case 2: st = launch_nt<XT, 2>(q, group, zeros, stream); break;
-      case 3: st = launch_nt<XT, 3>(q, group, zeros, stream); break;
-      default: st = launch_nt<XT, 4>(q, group, zeros, stream); break;
+    switch ((q.M * parts<XT>() + 7) / 8) {
+      case 1: st = launch_nt<XT, 1>(q, group, zeros, sms, stream); break;
+      case 2: st = launch_nt<XT, 2>(q, group, zeros, sms, stream); break;
+      case 3: st = launch_nt<XT, 3>(q, group, zeros, sms, stream); break;
+      default: st = launch_nt<XT, 4>(q, group, zeros, sms, stream); break;
     }
     if (st) return st;
   }
@@ -352,10 +693,13 @@ int launch_w4_prepare(const uint8_t* codes, int64_t ldc, const uint16_t* scales,
 int launch_w4_mmv(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t N, int64_t K,
                   int group, bool zeros, const uint8_t* plane, void* y, int y_dtype,
                   int overlap, int sm_count, cudaStream_t stream) {
-  W4Params p{x, plane, y, ldx, N, (int)M, (int)K, (int)((K + kUnitK - 1) / kUnitK), y_dtype};
-  if (x_dtype == PQ2_BF16) return launch_x<__nv_bfloat16>(p, M, group, zeros, stream);
-  if (x_dtype == PQ2_F16) return launch_x<__half>(p, M, group, zeros, stream);
-  return launch_x<float>(p, M, group, zeros, stream);
+  const int64_t tiles = (N + kTileRows - 1) / kTileRows;
+  W4Params p{};
+  p.x = x, p.plane = plane, p.y = y, p.ldx = ldx, p.N = N, p.K = (int)K, p.y_dtype = y_dtype;
+  p.tiles = (int)tiles, p.units = (int)((K + kUnitK - 1) / kUnitK), p.overlap = overlap;
+  if (x_dtype == PQ2_BF16) return launch_x<__nv_bfloat16>(p, M, group, zeros, sm_count, stream);
+  if (x_dtype == PQ2_F16) return launch_x<__half>(p, M, group, zeros, sm_count, stream);
+  return launch_x<float>(p, M, group, zeros, sm_count, stream);
 }
 
 }  // namespace pq2
