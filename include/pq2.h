@@ -618,7 +618,7 @@ int pq2_token_logprobs(const void *logits, int dtype, int64_t ldl, int64_t M,
  *        is NULL)
  *   h' = h + alpha * gate * p         (no gate if NULL; h' = h if z is NULL)
  *   n  = h' / sqrt(mean h'^2 + eps) * (w_pre + w_offset)
- * in fp32 with IEEE square roots and divisions; h' is rounded for h_out only.
+ * in fp32 (1 / sqrt is CUDA's rsqrtf, 2 ulp); h' is rounded for h_out only.
  *   z, h     (device) dtype [M][ldz], [M][ldh], both strides >= K; z NULL
  *            gives the plain norm of h (then no w_post, gate or h_out).
  *   w_post, w_pre (device) dtype [K]; w_pre may be NULL if n_out is.

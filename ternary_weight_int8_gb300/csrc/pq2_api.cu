@@ -721,9 +721,10 @@ int pq2_norm_gate_residual(const void* z, int64_t ldz, const void* h, int64_t ld
     return PQ2_ERR_ALIGN;
   int sms = 0;
   if (int st = device_check(&sms)) return st;
-  const pq2::NormParams p{z,   h,   w_pre, w_post, gate, h_out, n_out, ldz,
-                          ldh, ldg, rows_per_gate, M,    K,     alpha, eps, w_offset};
-  return pq2::launch_norm(p, dtype, sms, static_cast<cudaStream_t>(stream));
+  pq2::NormParams p{z, h, w_pre, w_post, gate, h_out, n_out, ldz, ldh, ldg, M, K};
+  p.rows_per_gate = (uint32_t)(rows_per_gate < M ? rows_per_gate : M);
+  p.alpha = alpha, p.eps = eps, p.w_offset = w_offset, p.one_over_k = 1.f / (float)K;
+  return pq2::launch_norm(p, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

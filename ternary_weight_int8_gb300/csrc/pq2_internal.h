@@ -113,9 +113,10 @@ int launch_token_logprobs(const void* logits, int dtype, int64_t ldl, int64_t M,
 struct NormParams {
   const void *z, *h, *w_pre, *w_post, *gate;
   void *h_out, *n_out;
-  int64_t ldz, ldh, ldg, rows_per_gate, M, K;
-  float alpha, eps, w_offset;
+  int64_t ldz, ldh, ldg, M, K;
+  uint32_t rows_per_gate;
+  float alpha, eps, w_offset, one_over_k;
 };
-int launch_norm(const NormParams& p, int dtype, int sm_count, cudaStream_t stream);
+int launch_norm(const NormParams& p, int dtype, cudaStream_t stream);
 
 }  // namespace pq2

@@ -586,9 +586,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
 template <typename XT, bool TOP>
 int launch_one(LogprobParams p, int64_t M, int sms, cudaStream_t stream) {
   auto kern = logprobs_kernel<XT, TOP>;
-  // CTAs a row: enough to give every SM two, of at least 2048 elements each.
+  // CTAs a row: enough to give every SM one, of at least 2048 elements each.
+  // (32 rows of 131072: 10.3 us in 256 CTAs, 14.6 us in 512; 300 rows of 100003:
+  // 21 us in 300 CTAs, 20 us in 600.)
   p.split = 1;
-  while (p.split < kMaxCluster && M * p.split < 2 * sms && p.V / (2 * p.split) >= 2048)
+  while (p.split < kMaxCluster && M * p.split < sms && p.V / (2 * p.split) >= 2048)
     p.split *= 2;
   if (M * p.split > 0x7FFFFFFF) return PQ2_ERR_SHAPE;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
