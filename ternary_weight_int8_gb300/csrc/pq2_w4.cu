@@ -7,8 +7,8 @@
 // mma.sync.m16n8k16 takes it as the A operand:
 //   512 B   lane l's 16 bytes: words of MMA steps 0..3
 //   512 B   lane l's 16 bytes: words of MMA steps 4..7
-//   per group of the unit: 8 x (scale of row i, scale of row i + 8), fp16
-//   with zero points, per group: 8 x (zero of row i | zero of row i + 8 << 4)
+//   for i = 0..7, per group: (scale of row i, scale of row i + 8), fp16
+//   with zero points, for i, per group: zero of row i | zero of row i + 8 << 4
 //   padding to 16 bytes
 // Step 2j + h of lane 4i + t covers the columns b = 32 j + 8 t + 4 h, ..,
 // b + 3 of rows i and i + 8, so that every step lies in one group of 32 and a
@@ -84,13 +84,14 @@ __global__ void w4_prepare_kernel(W4PrepParams p) {
   const int64_t row_groups = p.K / p.group;
   uint16_t* scales = reinterpret_cast<uint16_t*>(out + kUnitCodeBytes);
   uint8_t* zeros = out + kUnitCodeBytes + groups * 32;
-  for (int e = lane; e < groups * 16; e += 32) {  // e = group, pair, half
-    const int64_t g = u * groups + e / 16, n = tile * kTileRows + (e % 16) / 2 + 8 * (e & 1);
+  for (int e = lane; e < groups * 16; e += 32) {  // e = pair, group, half
+    const int64_t g = u * groups + e / 2 % groups;
+    const int64_t n = tile * kTileRows + e / 2 / groups + 8 * (e & 1);
     scales[e] = g < row_groups && n < p.N ? p.scales[n * row_groups + g] : 0;
   }
   if (p.zeros)
-    for (int e = lane; e < groups * 8; e += 32) {
-      const int64_t g = u * groups + e / 8, n = tile * kTileRows + e % 8;
+    for (int e = lane; e < groups * 8; e += 32) {  // e = pair, group
+      const int64_t g = u * groups + e % groups, n = tile * kTileRows + e / groups;
       uint32_t z = 0;
       if (g < row_groups && n < p.N) z = p.zeros[n * row_groups + g] & 15u;
       if (g < row_groups && n + 8 < p.N) z |= (p.zeros[(n + 8) * row_groups + g] & 15u) << 4;
@@ -102,13 +103,15 @@ __global__ void w4_prepare_kernel(W4PrepParams p) {
 // Product.
 //
 // A CTA holds a range of tiles and a range of units (all of them, or its
-// share when a cluster splits K).  It runs the units in passes of one unit
-// per warp: a warp keeps its unit's x in registers (the B fragments) and
-// streams that unit of tile after tile through a private ring of cp.async
-// copies, so a weight byte is read once and x once per CTA.  The warps' scaled
-// sums of a tile meet in shared memory, where they are added in unit order.
-// The order of a y's additions is therefore: MMA steps of a group, groups of
-// a unit, units of a CTA's range in ascending order, ranges in cluster order.
+// share when a cluster splits K), taken in pairs from the range's start.  It
+// runs the pairs in passes of one per warp: a warp keeps its pair's x in
+// registers (the B fragments) and streams that pair of tile after tile through
+// a private ring of cp.async copies, so a weight byte is read once and x once
+// per CTA.  The warps' scaled sums of a tile meet in shared memory, where they
+// are added in the order of the pairs.
+// The order of a y's additions: MMA steps of a group, groups of a unit, the
+// two units of a pair, pairs of a CTA's range in ascending order, ranges in
+// cluster order.
 
 struct W4Params {
   const void* x;
@@ -218,16 +221,18 @@ __device__ __forceinline__ void load8(const XT* x, bool vec, float* v) {
   }
 }
 
-// The B fragments of column `part` of row x (null: zeros) over one unit, and
-// the factor that undoes their scaling.  Every lane of the warp calls it; the
-// four lanes of a column agree on the scaling.
+// The B fragments of column `part` of row x (null: zeros) over one pair of
+// units from column k (this lane's first), and the factor that undoes their
+// scaling.  Every lane of the warp calls it; the four lanes of a column agree
+// on the scaling.
 template <typename XT>
-__device__ __forceinline__ float load_b(const XT* x, int k, int K, int part, bool vec, uint4* b) {
+__device__ __forceinline__ float load_b(const XT* x, int64_t k, int64_t K, int part, bool vec,
+                                        uint4* b) {
   if constexpr (std::is_same<XT, __half>::value) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       b[j] = make_uint4(0, 0, 0, 0);
-      if (x && k + 32 * j < K) {
+      if (x && k + 32 * j < K) {  // K is a multiple of 32
         if (vec) {
           b[j] = *reinterpret_cast<const uint4*>(x + k + 32 * j);
         } else {
@@ -239,15 +244,15 @@ __device__ __forceinline__ float load_b(const XT* x, int k, int K, int part, boo
     }
     return 1.f;
   } else {
-    float v[4][8];
+    // Twice through x (from L1 the second time): the values themselves would
+    // take 64 registers.
     float most = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
+      float v[8] = {};
+      if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = 0.f;
-      if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v[j]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[j][e]));
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
     }
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -255,11 +260,13 @@ __device__ __forceinline__ float load_b(const XT* x, int k, int K, int part, boo
     const int up = e8 == 255 ? 127 : min(268 - e8, 254);  // 2^(14 - exponent), as a biased exponent
     const float scale = __uint_as_float((uint32_t)up << 23);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
+      float v[8] = {};
+      if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v);
       uint32_t r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float f0 = v[j][2 * e] * scale, f1 = v[j][2 * e + 1] * scale;
+        float f0 = v[2 * e] * scale, f1 = v[2 * e + 1] * scale;
         if (part) {
           f0 -= __half2float(__float2half_rn(f0));
           f1 -= __half2float(__float2half_rn(f1));
@@ -271,25 +278,6 @@ __device__ __forceinline__ float load_b(const XT* x, int k, int K, int part, boo
     return up == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - up) << 23);
   }
 }
-
-__device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v) {
-  if (dtype == PQ2_F32) reinterpret_cast<float*>(y)[at] = v;
-  else if (dtype == PQ2_BF16) reinterpret_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
-  else reinterpret_cast<__half*>(y)[at] = __float2half(v);
-}
-
-constexpr int kPitch = 20;  // floats per column of 16 rows: conflict-free
-
-// Shape of a CTA by its MMA column tiles: warps (one unit each at a time),
-// CTAs an SM holds (registers and shared memory are bounded for that) and
-// ring stages.
-constexpr int kWarps = 8;
-template <int NT>
-struct Shape {
-  static constexpr int kPerSm = NT == 1 ? 3 : 2;
-  static constexpr int kStages = NT == 1 ? 5 : 4;
-  static constexpr int kSmem = (227 * 1024 - kPerSm * 1024) / kPerSm / 1024 * 1024;
-};
 
 // Shared memory by 32-bit address, and predicated without a branch: the loop
 // over tiles is bound by the instructions it issues.
@@ -313,17 +301,98 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t at) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
 __device__ __forceinline__ void sts_if(bool on, uint32_t at, float v) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.shared.f32 [%0], %1;\n\t}" ::"r"(at),
       "f"(v), "r"((int)on)
       : "memory");
 }
+
+// The scales and zero points of lane row pair i, per group of a unit.
+template <int GROUP, bool ZEROS>
+struct Side {
+  static constexpr int kGroups = kUnitK / GROUP;
+  uint32_t scale[kGroups], zero;
+  __device__ __forceinline__ void load(uint32_t unit, int i) {
+    const uint32_t at = unit + kUnitCodeBytes + i * 4 * kGroups;
+    if constexpr (kGroups == 1) scale[0] = lds32(at);
+    if constexpr (kGroups == 2)
+      asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(scale[0]), "=r"(scale[1]) : "r"(at) : "memory");
+    if constexpr (kGroups == 4) {
+      const uint4 v = lds128(at);
+      scale[0] = v.x, scale[1] = v.y, scale[2] = v.z, scale[3] = v.w;
+    }
+    if constexpr (ZEROS) {
+      const uint32_t z = unit + kUnitCodeBytes + 32 * kGroups + i * kGroups;
+      if constexpr (kGroups == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(zero) : "r"(z) : "memory");
+      if constexpr (kGroups == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(zero) : "r"(z) : "memory");
+      if constexpr (kGroups == 4) zero = lds32(z);
+    }
+  }
+  __device__ __forceinline__ float2 scales(int g) const { return __half22float2(half2_of(scale[g])); }
+  __device__ __forceinline__ uint32_t low(int g) const { return ZEROS ? zero >> 8 * g & 15 : 8; }
+  __device__ __forceinline__ uint32_t high(int g) const { return ZEROS ? zero >> (8 * g + 4) & 15 : 8; }
+};
+
+// One unit's products with the columns b[nt][j], scaled by the groups' scales:
+// sum = ADD ? sum + unit : unit.
+template <int NT, int GROUP, bool ZEROS, bool ADD, int BJ>
+__device__ __forceinline__ void unit_product(uint32_t unit, int lane, const uint4 (&b)[NT][BJ], int j0,
+                                             float (&sum)[NT][4]) {
+  constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
+  Side<GROUP, ZEROS> side;
+  side.load(unit, lane >> 2);
+  uint4 c;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const float2 s = side.scales(g);
+    const Offset o0 = offset_of(side.low(g)), o1 = offset_of(side.high(g));
+    float d[NT][4];
+#pragma unroll
+    for (int s2 = 0; s2 < kSteps; ++s2) {
+      const int step = g * kSteps + s2;
+      if (step % 4 == 0) c = lds128(unit + lane * 16 + step / 4 * 512);
+      const uint32_t w = step % 4 == 0 ? c.x : step % 4 == 1 ? c.y : step % 4 == 2 ? c.z : c.w;
+      uint32_t a[4];
+      decode(w, o0.low, o1.high, a);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 bb = b[nt][j0 + step / 2];
+        if (s2 == 0)
+          mma16816<true>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
+        else
+          mma16816<false>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float sc = e < 2 ? s.x : s.y;
+        sum[nt][e] = g == 0 && !ADD ? __fmul_rn(sc, d[nt][e]) : __fmaf_rn(sc, d[nt][e], sum[nt][e]);
+      }
+  }
+}
+
+__device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v) {
+  if (dtype == PQ2_F32) reinterpret_cast<float*>(y)[at] = v;
+  else if (dtype == PQ2_BF16) reinterpret_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
+  else reinterpret_cast<__half*>(y)[at] = __float2half(v);
+}
+
+constexpr int kPitch = 20;  // floats per column of 16 rows: conflict-free
+
+// Shape of a CTA by its MMA column tiles: warps (one pair of units each at a
+// time; a multiple of four, as an SM's four schedulers take warps in turn),
+// CTAs an SM holds (registers and shared memory are bounded for that) and ring
+// stages.
+constexpr int kWarps = 4;
+template <int NT>
+struct Shape {
+  static constexpr int kPerSm = NT == 1 ? 5 : 3;
+  static constexpr int kStages = 4;
+  static constexpr int kSmem = (227 * 1024 - kPerSm * 1024) / kPerSm / 1024 * 1024;
+};
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -337,16 +406,15 @@ template <typename XT, int NT, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(const W4Params p) {
   constexpr int kParts = parts<XT>();
   constexpr bool kScaled = !std::is_same<XT, __half>::value;
-  constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
   constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
+  constexpr int kSlot = 2 * kUnitBytes;
   constexpr int kStages = Shape<NT>::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
 
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, t = lane & 3;
   const int cols = p.M * kParts;
-  uint8_t* const ring = smem + warp * (kStages * kUnitBytes);
-  float* const red = reinterpret_cast<float*>(smem + warps * (kStages * kUnitBytes));
+  float* const red = reinterpret_cast<float*>(smem + warps * (kStages * kSlot));
   const int red_warp = cols * kPitch, red_tile = warps * red_warp;
   const int red_buf = red_tile << p.batch_log;
   float* const acc = red + 2 * red_buf;
@@ -357,67 +425,70 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
   const int t1 = (int)((int64_t)(cluster + 1) * p.tiles / clusters);
   const int u0 = (int)((int64_t)rank * p.units / p.split);
   const int u1 = (int)((int64_t)(rank + 1) * p.units / p.split);
+  const int pairs = (u1 - u0 + 1) / 2;
   const int64_t tile_bytes = (int64_t)p.units * kUnitBytes;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!p.overlap) dependency_wait();
 
   // The copies run kStages - 1 items ahead; items are (block of tiles, pass,
-  // tile), the last fastest.  `left`: tiles left of the pass being copied.
-  const uint32_t ring_end = smem_u32(ring) + kStages * kUnitBytes;
-  uint32_t dst = smem_u32(ring);
-  int lb = t0, left = min(p.block_tiles, t1 - t0), lu = u0 + warp;
-  bool go = lu < u1;
-  const uint8_t* src = p.plane + lb * tile_bytes + (int64_t)lu * kUnitBytes + lane * 16;
+  // tile), the last fastest.  `left`: tiles left of the pass being copied;
+  // `chunks`: what of an item this warp has (0: nothing).
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * kSlot), ring_end = ring + kStages * kSlot;
+  int lb = t0, left = min(p.block_tiles, t1 - t0), lp = warp;
+  auto chunks_of = [&](int pair) {
+    return pair >= pairs ? 0 : u0 + 2 * pair + 1 < u1 ? 2 * kChunks : kChunks;
+  };
+  int chunks = chunks_of(lp) - lane;
+  const uint8_t* src = p.plane + lb * tile_bytes + (int64_t)(u0 + 2 * lp) * kUnitBytes + lane * 16;
   auto copy_next = [&](uint32_t slot) {
     const uint32_t at = slot + lane * 16;
-    cp_async16_if(go, at, src);
-    cp_async16_if(go, at + 512, src + 512);
-    cp_async16_if(go && lane < kChunks - 64, at + 1024, src + 1024);
+#pragma unroll
+    for (int j = 0; j < (2 * kChunks + 31) / 32; ++j)
+      cp_async16_if(chunks > 32 * j, at + 512 * j, src + 512 * j);
     asm volatile("cp.async.commit_group;" ::: "memory");
     src += tile_bytes;
     if (--left == 0) {
-      lu += warps;
-      if (lu - warp >= u1) {
-        lu = u0 + warp;
+      lp += warps;
+      if (lp - warp >= pairs) {
+        lp = warp;
         lb += p.block_tiles;
       }
       left = min(p.block_tiles, t1 - lb);
-      go = lu < u1 && left > 0;
-      src = p.plane + lb * tile_bytes + (int64_t)lu * kUnitBytes + lane * 16;
+      chunks = left > 0 ? chunks_of(lp) - lane : 0;
+      src = p.plane + lb * tile_bytes + (int64_t)(u0 + 2 * lp) * kUnitBytes + lane * 16;
     }
   };
+  uint32_t dst = ring;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     copy_next(dst);
-    dst += kUnitBytes;
+    dst += kSlot;
   }
   if (p.overlap == 1) dependency_wait();
 
   // dst: the slot that the item before the current one used; cur: its own.
-  uint32_t cur = smem_u32(ring);
-  bool on[NT][2];  // which of its MMA columns exist
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    on[nt][0] = 8 * nt + 2 * t < cols;
-    on[nt][1] = 8 * nt + 2 * t + 1 < cols;
-  }
+  uint32_t cur = ring;
   const uint32_t out0 = smem_u32(red + warp * red_warp + 2 * t * kPitch + i);
-  uint4 b[NT][4];
+  uint4 b[NT][8];
   float undo[NT][2];
   int buf = 0;
   bool waited = p.overlap != 2;
   for (int b0 = t0; b0 < t1; b0 += p.block_tiles) {
     const int b1 = min(b0 + p.block_tiles, t1);
-    for (int pu = u0; pu < u1 || pu == u0; pu += warps) {
-      const int u = pu + warp, active = min(warps, u1 - pu);
-      const bool last = pu + warps >= u1, idle = u >= u1;
-      if (!idle && (b0 == t0 || u1 - u0 > warps)) {
+    for (int pp = 0; pp < pairs || pp == 0; pp += warps) {
+      const int pair = pp + warp, active = min(warps, pairs - pp);
+      const bool last = pp + warps >= pairs, idle = pair >= pairs;
+      const bool two = u0 + 2 * pair + 1 < u1;
+      if (!idle && (b0 == t0 || pairs > warps)) {
+        // A unit beyond the range belongs to another CTA.
+        const int64_t end = min((int64_t)p.K, (int64_t)u1 * kUnitK);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int v = 8 * nt + i, m = v / kParts;
           const XT* x = m < p.M ? static_cast<const XT*>(p.x) + m * p.ldx : nullptr;
-          const float f = load_b(x, u * kUnitK + 8 * t, p.K, v % kParts, p.vector_x != 0, b[nt]);
+          const float f = load_b(x, (int64_t)(u0 + 2 * pair) * kUnitK + 8 * t, end, v % kParts,
+                                 p.vector_x != 0, b[nt]);
           if (kScaled) {
             undo[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
             undo[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
@@ -431,7 +502,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
           for (int tile = tb; tile < te; ++tile) {
             copy_next(dst);
             dst = cur;
-            cur = cur + kUnitBytes == ring_end ? ring_end - kStages * kUnitBytes : cur + kUnitBytes;
+            cur = cur + kSlot == ring_end ? ring : cur + kSlot;
           }
         } else {
 #pragma unroll 1
@@ -440,59 +511,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
             __syncwarp();
             copy_next(dst);
             dst = cur;
-            const uint32_t codes = cur + lane * 16, side = cur + kUnitCodeBytes + i * 4;
-            cur += kUnitBytes;
-            cur = cur == ring_end ? ring_end - kStages * kUnitBytes : cur;
+            cur += kSlot;
+            cur = cur == ring_end ? ring : cur;
             float sum[NT][4];
-            uint4 c;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-              const float2 s = __half22float2(half2_of(lds32(side + 32 * g)));
-              Offset o0, o1;
-              if (ZEROS) {
-                const uint32_t z = lds8(dst + kUnitCodeBytes + 32 * kGroups + 8 * g + i);
-                o0 = offset_of(z & 15), o1 = offset_of(z >> 4);
-              } else {
-                o0 = o1 = offset_of(8);
-              }
-              float d[NT][4];
-#pragma unroll
-              for (int s2 = 0; s2 < kSteps; ++s2) {
-                const int step = g * kSteps + s2;
-                if (step % 4 == 0) c = lds128(codes + step / 4 * 512);
-                const uint32_t w = step % 4 == 0 ? c.x : step % 4 == 1 ? c.y : step % 4 == 2 ? c.z : c.w;
-                uint32_t a[4];
-                decode(w, o0.low, o1.high, a);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint4 bb = b[nt][step / 2];
-                  if (s2 == 0)
-                    mma16816<true>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
-                  else
-                    mma16816<false>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
-                }
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float sc = e < 2 ? s.x : s.y;
-                  sum[nt][e] = g == 0 ? sc * d[nt][e] : fmaf(sc, d[nt][e], sum[nt][e]);
-                }
-            }
+            unit_product<NT, GROUP, ZEROS, false>(dst, lane, b, 0, sum);
+            if (two) unit_product<NT, GROUP, ZEROS, true>(dst + kUnitBytes, lane, b, 4, sum);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t at = out + (8 * nt + h) * kPitch * 4;
-                sts_if(on[nt][h], at, kScaled ? sum[nt][h] * undo[nt][h] : sum[nt][h]);
-                sts_if(on[nt][h], at + 32, kScaled ? sum[nt][h + 2] * undo[nt][h] : sum[nt][h + 2]);
+                const bool on = 8 * nt + 2 * t + h < cols;
+                sts_if(on, at, kScaled ? __fmul_rn(sum[nt][h], undo[nt][h]) : sum[nt][h]);
+                sts_if(on, at + 32, kScaled ? __fmul_rn(sum[nt][h + 2], undo[nt][h]) : sum[nt][h + 2]);
               }
             out += red_tile * 4;
           }
         }
         __syncthreads();
-        // Join: one thread per (column, row of the batch), in unit order.
+        // Join: one thread per (column, row of the batch), in the order of the pairs.
         const bool done = last && p.split == 1 && kParts == 1;
         if (done && !waited) {
           dependency_wait();
@@ -504,8 +541,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
           if (r >= rows) continue;
           float* a = acc + (v * p.block_tiles + tb - b0) * kTileRows + r;
           const float* q = red + buf * red_buf + (r >> 4) * red_tile + v * kPitch + (r & 15);
-          float sum = pu == u0 ? 0.f : *a;
-#pragma unroll 5
+          float sum = pp == 0 ? 0.f : *a;
+#pragma unroll 4
           for (int w = 0; w < active; ++w) sum += q[w * red_warp];
           if (done) {
             const int64_t n = (int64_t)tb * kTileRows + r;
@@ -563,13 +600,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
 // The split of K over a cluster orders the additions, so it depends on the
 // matrix and the SM count only.  A CTA's time is its passes times (its tiles +
 // the start of a pass, worth about 6 tiles), and a cluster's join is worth
-// about 4 more; taken where that is least, for three CTAs an SM.
+// about 4 more; taken where that is least, for a full device.
 int w4_split(int tiles, int units, int sms) {
   int split = 1;
   int64_t least = INT64_MAX;
   for (int c = 1; c <= 8 && c <= units; ++c) {
-    const int share = (units + c - 1) / c, passes = (share + kWarps - 1) / kWarps;
-    const int clusters = std::max(1, 3 * sms / c);
+    const int pairs = ((units + c - 1) / c + 1) / 2, passes = (pairs + kWarps - 1) / kWarps;
+    const int clusters = std::max(1, Shape<1>::kPerSm * sms / c);
     const int64_t cost = (int64_t)passes * ((tiles + clusters - 1) / clusters + 6) + (c > 1 ? 4 : 0);
     if (cost < least) least = cost, split = c;
   }
@@ -586,9 +623,8 @@ int launch_one(W4Params p, int sms, cudaStream_t stream) {
   static std::atomic<int> resident[64][9];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PQ2_ERR_CUDA;
-  const int share = (p.units + p.split - 1) / p.split;
-  const int passes = (share + kWarps - 1) / kWarps;
-  const int warps = (share + passes - 1) / passes;
+  const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
+  const int warps = std::min(kWarps, pairs);
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = S::kSmem;
@@ -616,11 +652,11 @@ int launch_one(W4Params p, int sms, cudaStream_t stream) {
   const int each = (p.tiles + most - 1) / most;
   const int clusters = (p.tiles + each - 1) / each;
   const int cols = p.M * parts<XT>();
-  const int ring = warps * S::kStages * unit_bytes(GROUP, ZEROS);
+  const int ring = warps * S::kStages * 2 * unit_bytes(GROUP, ZEROS);
   const int red_tile = warps * cols * kPitch * 4, acc_tile = cols * kTileRows * 4;
   const auto red = [&](int log) { return 2 * (red_tile << log); };
   p.batch_log = 0;
-  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= 24 * 1024 &&
+  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= 8 * 1024 &&
          ring + red(p.batch_log + 1) + 4 * acc_tile <= S::kSmem)
     ++p.batch_log;
   p.block_tiles = std::min(each, (S::kSmem - ring - red(p.batch_log)) / acc_tile);
@@ -651,8 +687,8 @@ int launch_nt(const W4Params& p, int group, bool zeros, int sms, cudaStream_t st
 
 template <typename XT>
 int launch_x(W4Params p, int64_t M, int group, bool zeros, int sms, cudaStream_t stream) {
-  // At most 32 MMA columns at a time: 32 columns of x, or 16 of a 32-bit x.
-  constexpr int kMost = 32 / parts<XT>();
+  // At most 16 MMA columns at a time: 16 columns of x, or 8 of a 32-bit x.
+  constexpr int kMost = 16 / parts<XT>();
   const int y_size = p.y_dtype == PQ2_F32 ? 4 : 2;
   p.vector_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(XT) % 16 == 0;
   for (int64_t m = 0; m < M; m += kMost) {
@@ -661,12 +697,8 @@ int launch_x(W4Params p, int64_t M, int group, bool zeros, int sms, cudaStream_t
     q.x = static_cast<const XT*>(p.x) + m * p.ldx;
     q.y = static_cast<uint8_t*>(p.y) + m * p.N * y_size;
     int st;
-    switch ((q.M * parts<XT>() + 7) / 8) {
-      case 1: st = launch_nt<XT, 1>(q, group, zeros, sms, stream); break;
-      case 2: st = launch_nt<XT, 2>(q, group, zeros, sms, stream); break;
-      case 3: st = launch_nt<XT, 3>(q, group, zeros, sms, stream); break;
-      default: st = launch_nt<XT, 4>(q, group, zeros, sms, stream); break;
-    }
+    st = q.M * parts<XT>() <= 8 ? launch_nt<XT, 1>(q, group, zeros, sms, stream)
+                                : launch_nt<XT, 2>(q, group, zeros, sms, stream);
     if (st) return st;
   }
   return PQ2_OK;

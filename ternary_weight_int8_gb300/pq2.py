@@ -123,10 +123,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object (3 us a call, as much as a
+# whole small kernel); the raw handle is what the library takes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 _DT = {torch.bfloat16: PQ2_BF16, torch.float16: PQ2_F16, torch.float32: PQ2_F32}
@@ -507,6 +515,14 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
     return plane
 
 
+_w4_bytes = {}
+
+
+def _check_out(t, shape, *dtypes):
+    if t.shape != shape or not t.is_contiguous() or (dtypes and t.dtype not in dtypes):
+        raise ValueError(f"Expected a contiguous output buffer of shape {shape}")
+
+
 def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
                out_dtype=torch.float32, flags=0, stream=None):
     """y[M][N] = x W^T for M = 1..32 on a plane of N rows from pq2_w4_prepare
@@ -516,6 +532,13 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
     M, K = x.shape
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    else:
+        _check_out(y, (M, N))
+    key = (N, K, group, zeros)
+    if key not in _w4_bytes:
+        _w4_bytes[key] = lib().pq2_w4_plane_bytes(N, K, group, int(zeros))
+    if plane.numel() < _w4_bytes[key]:
+        raise Pq2Error("pq2_w4_mmv", PQ2_ERR_SHAPE)
     _check("pq2_w4_mmv", lib().pq2_w4_mmv(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, group, int(zeros), _ptr(plane), _ptr(y),
         _DT[y.dtype], flags, _stream(stream)))
@@ -540,6 +563,12 @@ def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entr
                torch.empty((M,), dtype=torch.float32, device=dev) if entropy else None,
                torch.empty((M, k), dtype=torch.int64, device=dev),
                torch.empty((M, k), dtype=torch.float32, device=dev))
+    else:
+        _check_out(out[0], (M, T), torch.float32)
+        if out[1] is not None:
+            _check_out(out[1], (M,), torch.float32)
+        _check_out(out[2], (M, k), torch.int64)
+        _check_out(out[3], (M, k), torch.float32)
     _check("pq2_token_logprobs", lib().pq2_token_logprobs(
         _ptr(logits), _DT[logits.dtype], logits.stride(0), M, V, scale, _ptr(tokens), T,
         _ptr(out[0]) if T else None, _ptr(out[1]), k, _ptr(out[2]) if k else None,
@@ -554,25 +583,36 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
     h' = h + alpha * gate * norm(z, w_post), n = norm(h', w_pre) ->
     (h_out, n_out).  z None: the plain norm of h (h_out None); w_pre None: no
     n_out.  All tensors have h's type."""
-    for t in (z, h, gate):
-        if t is not None and (t.dim() != 2 or t.stride(1) != 1 or t.dtype != h.dtype):
-            raise ValueError("z, h and gate must be 2-D of one type with unit column stride")
-    M, K = h.shape
-    if z is not None and z.shape != h.shape:
-        raise ValueError("z and h must have one shape")
-    if gate is not None and (gate.shape[1] != K or gate.shape[0] * rows_per_gate < M):
-        raise ValueError("gate must have K columns and a row per rows_per_gate rows of h")
-    for t in (w_pre, w_post):
-        if t is not None and (t.shape != (K,) or t.dtype != h.dtype or not t.is_contiguous()):
+    dtype = h.dtype
+    if h.dim() != 2 or h.stride(1) != 1:
+        raise ValueError("h must be 2-D with unit column stride")
+    M, K = shape = h.shape
+    ldz = ldg = 0
+    if z is not None:
+        if z.shape != shape or z.dtype != dtype or z.stride(1) != 1:
+            raise ValueError("z must have h's shape and type and unit column stride")
+        ldz = z.stride(0)
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[1] != K or gate.shape[0] * rows_per_gate < M or \
+                gate.dtype != dtype or gate.stride(1) != 1:
+            raise ValueError("gate must have h's type, K columns with unit stride and a row per "
+                             "rows_per_gate rows of h")
+        ldg = gate.stride(0)
+    for w in (w_pre, w_post):
+        if w is not None and (w.numel() != K or w.dtype != dtype or not w.is_contiguous()):
             raise ValueError("the norm weights must be contiguous [K] of h's type")
-    if h_out is None and z is not None:
-        h_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
-    if n_out is None and w_pre is not None:
-        n_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
+    if h_out is not None:
+        _check_out(h_out, shape, dtype)
+    elif z is not None:
+        h_out = torch.empty((M, K), dtype=dtype, device=h.device)
+    if n_out is not None:
+        _check_out(n_out, shape, dtype)
+    elif w_pre is not None:
+        n_out = torch.empty((M, K), dtype=dtype, device=h.device)
     _check("pq2_norm_gate_residual", lib().pq2_norm_gate_residual(
-        _ptr(z), 0 if z is None else z.stride(0), _ptr(h), h.stride(0), _DT[h.dtype],
-        _ptr(w_post), _ptr(gate), 0 if gate is None else gate.stride(0), rows_per_gate, alpha,
-        _ptr(w_pre), w_offset, eps, M, K, _ptr(h_out), _ptr(n_out), _stream(stream)))
+        _ptr(z), ldz, _ptr(h), h.stride(0), _DT[dtype], _ptr(w_post), _ptr(gate), ldg,
+        rows_per_gate, alpha, _ptr(w_pre), w_offset, eps, M, K, _ptr(h_out), _ptr(n_out),
+        _stream(stream)))
     return h_out, n_out
 
 
