@@ -190,33 +190,30 @@ __device__ __forceinline__ void decode(uint32_t w, __half2 low, __half2 high, ui
   a[3] = bits(__hfma2(field(v, 0x00F000F0u), sixteenth, high));
 }
 
-// 8 consecutive elements of x in fp32.
-template <typename XT>
-__device__ __forceinline__ void load8(const XT* x, bool vec, float* v) {
-  if constexpr (std::is_same<XT, float>::value) {
-    if (vec) {
-      const float4 lo = reinterpret_cast<const float4*>(x)[0];
-      const float4 hi = reinterpret_cast<const float4*>(x)[1];
-      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-      v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-      return;
-    }
+// 8 consecutive elements of a 32-bit x.
+__device__ __forceinline__ void load8(const float* x, bool vec, float* v) {
+  if (vec) {
+    const float4 lo = reinterpret_cast<const float4*>(x)[0];
+    const float4 hi = reinterpret_cast<const float4*>(x)[1];
+    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+    return;
+  }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = x[e];
-  } else {
-    uint32_t w[4];
-    if (vec) {
-      const uint4 q = *reinterpret_cast<const uint4*>(x);
-      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-    } else {
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(x);
+  for (int e = 0; e < 8; ++e) v[e] = x[e];
+}
+// 8 consecutive elements of a 16-bit x in each 32-group of a pair of units.
+__device__ __forceinline__ void load_raw(const uint16_t* x, int64_t k, int64_t K, bool vec, uint4* b) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = q[2 * e] | (uint32_t)q[2 * e + 1] << 16;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  for (int j = 0; j < 8; ++j) {
+    b[j] = make_uint4(0, 0, 0, 0);
+    if (x && k + 32 * j < K) {  // K is a multiple of 32
+      const uint16_t* q = x + k + 32 * j;
+      if (vec)
+        b[j] = *reinterpret_cast<const uint4*>(q);
+      else
+        b[j] = make_uint4(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16,
+                          q[4] | (uint32_t)q[5] << 16, q[6] | (uint32_t)q[7] << 16);
     }
   }
 }
@@ -229,28 +226,32 @@ template <typename XT>
 __device__ __forceinline__ float load_b(const XT* x, int64_t k, int64_t K, int part, bool vec,
                                         uint4* b) {
   if constexpr (std::is_same<XT, __half>::value) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      b[j] = make_uint4(0, 0, 0, 0);
-      if (x && k + 32 * j < K) {  // K is a multiple of 32
-        if (vec) {
-          b[j] = *reinterpret_cast<const uint4*>(x + k + 32 * j);
-        } else {
-          const uint16_t* q = reinterpret_cast<const uint16_t*>(x + k + 32 * j);
-          b[j] = make_uint4(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16,
-                            q[4] | (uint32_t)q[5] << 16, q[6] | (uint32_t)q[7] << 16);
-        }
-      }
-    }
+    load_raw(reinterpret_cast<const uint16_t*>(x), k, K, vec, b);
     return 1.f;
   } else {
-    // Twice through x (from L1 the second time): the values themselves would
-    // take 64 registers.
+    // bf16 stays in its registers until it is scaled; a 32-bit x is read twice
+    // (from L1 the second time), as its values would take 64 registers.
+    constexpr bool kKeep = !std::is_same<XT, float>::value;
+    auto get = [&](int j, float* v) {
+      if constexpr (kKeep) {
+        const uint32_t w[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = __uint_as_float(w[e] << 16);
+          v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v);
+      }
+    };
+    if constexpr (kKeep) load_raw(reinterpret_cast<const uint16_t*>(x), k, K, vec, b);
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float v[8] = {};
-      if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v);
+      float v[8];
+      get(j, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
     }
@@ -261,8 +262,8 @@ __device__ __forceinline__ float load_b(const XT* x, int64_t k, int64_t K, int p
     const float scale = __uint_as_float((uint32_t)up << 23);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float v[8] = {};
-      if (x && k + 32 * j < K) load8(x + k + 32 * j, vec, v);
+      float v[8];
+      get(j, v);
       uint32_t r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -382,17 +383,11 @@ __device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v)
 
 constexpr int kPitch = 20;  // floats per column of 16 rows: conflict-free
 
-// Shape of a CTA by its MMA column tiles: warps (one pair of units each at a
-// time; a multiple of four, as an SM's four schedulers take warps in turn),
-// CTAs an SM holds (registers and shared memory are bounded for that) and ring
-// stages.
-constexpr int kWarps = 4;
-template <int NT>
-struct Shape {
-  static constexpr int kPerSm = NT == 1 ? 5 : 3;
-  static constexpr int kStages = 4;
-  static constexpr int kSmem = (227 * 1024 - kPerSm * 1024) / kPerSm / 1024 * 1024;
-};
+// The narrow kernel's CTA: warps (one pair of units each at a time; a multiple
+// of four, as an SM's four schedulers take warps in turn), CTAs an SM holds
+// (registers and shared memory are bounded for that) and ring stages.
+constexpr int kWarps = 4, kPerSm = 4, kStages = 3;
+constexpr int kSmem = (227 / kPerSm - 1) * 1024;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -403,12 +398,11 @@ __device__ __forceinline__ void dependency_wait() {
 }
 
 template <typename XT, int NT, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(const W4Params p) {
+__global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Params p) {
   constexpr int kParts = parts<XT>();
   constexpr bool kScaled = !std::is_same<XT, __half>::value;
   constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
   constexpr int kSlot = 2 * kUnitBytes;
-  constexpr int kStages = Shape<NT>::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
 
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -495,6 +489,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
           }
         }
       }
+      // The fragments are values of their own from here on, not to be formed
+      // again from x inside the loop.
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          asm volatile("" : "+r"(b[nt][j].x), "+r"(b[nt][j].y), "+r"(b[nt][j].z), "+r"(b[nt][j].w));
       for (int tb = b0; tb < b1; tb += 1 << p.batch_log) {
         const int te = min(tb + (1 << p.batch_log), b1);
         uint32_t out = out0 + buf * red_buf * 4;
@@ -514,8 +515,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
             cur += kSlot;
             cur = cur == ring_end ? ring : cur;
             float sum[NT][4];
-            unit_product<NT, GROUP, ZEROS, false>(dst, lane, b, 0, sum);
-            if (two) unit_product<NT, GROUP, ZEROS, true>(dst + kUnitBytes, lane, b, 4, sum);
+            if (two) {
+              unit_product<NT, GROUP, ZEROS, false>(dst, lane, b, 0, sum);
+              unit_product<NT, GROUP, ZEROS, true>(dst + kUnitBytes, lane, b, 4, sum);
+            } else {
+              unit_product<NT, GROUP, ZEROS, false>(dst, lane, b, 0, sum);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -597,6 +602,259 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<NT>::kPerSm) w4_mmv_kernel(
   if (!waited) dependency_wait();
 }
 
+// The wide kernel, for 9 to 32 columns.  x fragments of that many columns do
+// not fit a warp's registers, so a CTA keeps those of its range of units in
+// shared memory, and a warp takes two tiles through the whole range: each
+// fragment it loads serves both, and its sums need no join within the CTA.
+// The ranges of a cluster are joined round by round by warps of their own,
+// while the others are at the next round: a cluster barrier a round, two sets
+// of sums.  The order of the additions is the narrow kernel's.
+constexpr int kWideWarps = 8, kJoinWarps = 4, kWideStages = 4;
+constexpr int kRoundTiles = 2 * kWideWarps;
+constexpr int kRoundRows = kRoundTiles * kTileRows;
+constexpr int kRoundPitch = kRoundRows + 4;  // floats per column: conflict-free
+constexpr int kWideSmem = 227 * 1024;
+
+template <int NT>
+constexpr int wide_smem(int pairs, int unit_b) {
+  return kWideWarps * kWideStages * 2 * unit_b + pairs * 8 * NT * 512 +
+         (pairs + 2 * kRoundPitch) * 8 * NT * 4;
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float remote_float(const float* p, int rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .u32 at;\n\tmapa.shared::cluster.u32 at, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [at];\n\t}"
+      : "=f"(v)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// unit_product for two tiles, with the fragments from shared memory.
+template <int NT, int GROUP, bool ZEROS, bool ADD>
+__device__ __forceinline__ void unit_product2(const uint32_t (&unit)[2], int lane, uint32_t b_at,
+                                              float (&sum)[2][NT][4]) {
+  constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
+  Side<GROUP, ZEROS> side[2];
+  side[0].load(unit[0], lane >> 2);
+  side[1].load(unit[1], lane >> 2);
+  uint4 c[2], b[NT];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    float d[2][NT][4];
+#pragma unroll
+    for (int s2 = 0; s2 < kSteps; ++s2) {
+      const int step = g * kSteps + s2;
+      if (step % 4 == 0) {
+        c[0] = lds128(unit[0] + lane * 16 + step / 4 * 512);
+        c[1] = lds128(unit[1] + lane * 16 + step / 4 * 512);
+      }
+      if (step % 2 == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) b[nt] = lds128(b_at + (step / 2 * NT + nt) * 512);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = step % 4 == 0 ? c[h].x : step % 4 == 1 ? c[h].y : step % 4 == 2 ? c[h].z : c[h].w;
+        uint32_t a[4];
+        decode(w, offset_of(side[h].low(g)).low, offset_of(side[h].high(g)).high, a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (s2 == 0)
+            mma16816<true>(d[h][nt], a, step % 2 ? b[nt].z : b[nt].x, step % 2 ? b[nt].w : b[nt].y);
+          else
+            mma16816<false>(d[h][nt], a, step % 2 ? b[nt].z : b[nt].x, step % 2 ? b[nt].w : b[nt].y);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 s = side[h].scales(g);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float sc = e < 2 ? s.x : s.y;
+          sum[h][nt][e] = g == 0 && !ADD ? __fmul_rn(sc, d[h][nt][e])
+                                         : __fmaf_rn(sc, d[h][nt][e], sum[h][nt][e]);
+        }
+    }
+  }
+}
+
+template <typename XT, int NT, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_kernel(const W4Params p) {
+  constexpr int kParts = parts<XT>();
+  constexpr bool kScaled = !std::is_same<XT, __half>::value;
+  constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
+  constexpr int kCols = 8 * NT, kSlot = 2 * kUnitBytes;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane >> 2, t = lane & 3;
+
+  const int rank = blockIdx.x % p.split, cluster = blockIdx.x / p.split;
+  const int clusters = gridDim.x / p.split;
+  const int t0 = (int)((int64_t)cluster * p.tiles / clusters);
+  const int t1 = (int)((int64_t)(cluster + 1) * p.tiles / clusters);
+  const int u0 = (int)((int64_t)rank * p.units / p.split);
+  const int u1 = (int)((int64_t)(rank + 1) * p.units / p.split);
+  const int units = u1 - u0, pairs = (units + 1) / 2;
+  const int rounds = (t1 - t0 + kRoundTiles - 1) / kRoundTiles;
+  const int64_t tile_bytes = (int64_t)p.units * kUnitBytes;
+
+  uint8_t* const frag = smem + kWideWarps * kWideStages * kSlot;  // [pair][8][NT][32 lanes] 16 B
+  // The same places in every CTA of the cluster, whose ranges differ by a unit.
+  const int places = ((p.units + p.split - 1) / p.split + 1) / 2;
+  float* const undo = reinterpret_cast<float*>(frag + places * 8 * NT * 512);  // [pair][kCols]
+  float* const sums = undo + places * kCols;                                   // [2][kCols][pitch]
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!p.overlap) dependency_wait();
+
+  // The copies: items are (round, unit), both tiles of the warp's pair.
+  const uint32_t ring = smem_u32(smem) + warp * (kWideStages * kSlot);
+  int ct = t0 + 2 * warp, cu = 0;  // tile and unit of the next copy
+  auto copy_next = [&](uint32_t slot) {
+    if (ct < t1) {
+      const uint8_t* src = p.plane + ct * tile_bytes + (int64_t)(u0 + cu) * kUnitBytes + lane * 16;
+      const bool both = ct + 1 < t1;
+      const uint32_t at = slot + lane * 16;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        cp_async16_if(lane < kChunks - 32 * j, at + 512 * j, src + 512 * j);
+        cp_async16_if(both && lane < kChunks - 32 * j, at + kUnitBytes + 512 * j,
+                      src + tile_bytes + 512 * j);
+      }
+      if (++cu == units) {
+        cu = 0;
+        ct += kRoundTiles;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint32_t dst = ring;
+  if (warp < kWideWarps) {
+#pragma unroll
+    for (int s = 0; s < kWideStages - 1; ++s) {
+      copy_next(dst);
+      dst += kSlot;
+    }
+  }
+  if (p.overlap == 1) dependency_wait();
+
+  // x's fragments, once.
+  for (int task = warp; task < pairs * NT; task += kWideWarps + kJoinWarps) {
+    const int q = task / NT, nt = task % NT, v = 8 * nt + i, m = v / kParts;
+    const XT* x = m < p.M ? static_cast<const XT*>(p.x) + m * p.ldx : nullptr;
+    const int64_t end = min((int64_t)p.K, (int64_t)u1 * kUnitK);
+    uint4 b[8];
+    const float f = load_b(x, (int64_t)(u0 + 2 * q) * kUnitK + 8 * t, end, v % kParts,
+                           p.vector_x != 0, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<uint4*>(frag + ((q * 8 + j) * NT + nt) * 512 + lane * 16) = b[j];
+    if (t == 0) undo[q * kCols + v] = f;
+  }
+  __syncthreads();
+
+  if (warp < kWideWarps) {
+    const uint32_t ring_end = ring + kWideStages * kSlot;
+    uint32_t cur = ring;
+    for (int n = 0; n < rounds; ++n) {
+      const int tile = t0 + n * kRoundTiles + 2 * warp;
+      float acc[2][NT][4] = {};
+      if (tile < t1) {
+        const uint32_t second = tile + 1 < t1 ? kUnitBytes : 0;
+        float sum[2][NT][4];
+#pragma unroll 1
+        for (int q = 0; q < pairs; ++q) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (2 * q + h >= units) break;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kWideStages - 2) : "memory");
+            __syncwarp();
+            copy_next(dst);
+            dst = cur;
+            cur += kSlot;
+            cur = cur == ring_end ? ring : cur;
+            const uint32_t unit[2] = {dst, dst + second};
+            const uint32_t b_at = smem_u32(frag) + (q * 8 + 4 * h) * NT * 512 + lane * 16;
+            if (h == 0)
+              unit_product2<NT, GROUP, ZEROS, false>(unit, lane, b_at, sum);
+            else
+              unit_product2<NT, GROUP, ZEROS, true>(unit, lane, b_at, sum);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 f = *reinterpret_cast<const float2*>(undo + q * kCols + 8 * nt + 2 * t);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[h][nt][e] = __fadd_rn(
+                    acc[h][nt][e], kScaled ? __fmul_rn(sum[h][nt][e], e % 2 ? f.y : f.x) : sum[h][nt][e]);
+          }
+        }
+      }
+      if (n) cluster_wait();  // the sums of round n - 2 have been joined
+      float* s = sums + (n & 1) * kCols * kRoundPitch + 2 * t * kRoundPitch + 2 * warp * kTileRows + i;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[(8 * nt + e % 2) * kRoundPitch + h * kTileRows + e / 2 * 8] = acc[h][nt][e];
+      cluster_arrive();
+    }
+    if (rounds) cluster_wait();
+  } else {
+    if (p.overlap == 2) dependency_wait();
+    for (int n = 0; n < rounds; ++n) {
+      cluster_arrive();
+      cluster_wait();
+      // Parts of a 32-bit x (the smaller first) and ranges of the cluster.
+      const int64_t n0 = (int64_t)(t0 + n * kRoundTiles) * kTileRows;
+      const int rows = min(kRoundTiles, t1 - t0 - n * kRoundTiles) * kTileRows;
+      const float* s = sums + (n & 1) * kCols * kRoundPitch;
+      for (int e = threadIdx.x - kWideWarps * 32 + rank * kJoinWarps * 32; e < kRoundRows * p.M;
+           e += p.split * kJoinWarps * 32) {
+        const int m = e / kRoundRows, r = e % kRoundRows;
+        if (r >= rows || n0 + r >= p.N) continue;
+        float v[8][kParts];
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+          if (z < p.split) {
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+              v[z][q] = remote_float(s + (m * kParts + q) * kRoundPitch + r, z);
+          }
+        float y = 0.f;
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+          if (z < p.split) {
+            float sum = 0.f;
+#pragma unroll
+            for (int q = kParts - 1; q >= 0; --q) sum += v[z][q];
+            y += sum;
+          }
+        store_y(p.y, p.y_dtype, m * p.N + n0 + r, y);
+      }
+    }
+  }
+  // No CTA leaves while others read its sums.
+  cluster_arrive();
+  cluster_wait();
+  if (p.overlap == 2 && warp < kWideWarps) dependency_wait();
+}
+
 // The split of K over a cluster orders the additions, so it depends on the
 // matrix and the SM count only.  A CTA's time is its passes times (its tiles +
 // the start of a pass, worth about 6 tiles), and a cluster's join is worth
@@ -606,65 +864,55 @@ int w4_split(int tiles, int units, int sms) {
   int64_t least = INT64_MAX;
   for (int c = 1; c <= 8 && c <= units; ++c) {
     const int pairs = ((units + c - 1) / c + 1) / 2, passes = (pairs + kWarps - 1) / kWarps;
-    const int clusters = std::max(1, Shape<1>::kPerSm * sms / c);
+    const int clusters = std::max(1, kPerSm * sms / c);
     const int64_t cost = (int64_t)passes * ((tiles + clusters - 1) / clusters + 6) + (c > 1 ? 4 : 0);
     if (cost < least) least = cost, split = c;
   }
   return split;
 }
 
-template <typename XT, int NT, int GROUP, bool ZEROS>
-int launch_one(W4Params p, int sms, cudaStream_t stream) {
-  using S = Shape<NT>;
-  auto kern = w4_mmv_kernel<XT, NT, GROUP, ZEROS>;
-  p.split = w4_split(p.tiles, p.units, sms);
-
-  // Clusters that fit the device at once, looked up once per device.
-  static std::atomic<int> resident[64][9];
+// Clusters of `kern` that fit the device at once, looked up once per device
+// and cluster size.
+template <typename Kernel>
+int resident_clusters(Kernel kern, std::atomic<int> (&known)[64][9], int split, int threads,
+                      int smem, int* most) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PQ2_ERR_CUDA;
-  const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
-  const int warps = std::min(kWarps, pairs);
+  *most = known[dev][split].load(std::memory_order_acquire);
+  if (*most) return PQ2_OK;
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.gridDim = dim3(split);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(most, kern, &cfg) != cudaSuccess || *most < 1) {
+    cudaGetLastError();
+    return PQ2_ERR_CUDA;
+  }
+  known[dev][split].store(*most, std::memory_order_release);
+  return PQ2_OK;
+}
+
+template <typename Kernel>
+int launch(Kernel kern, const W4Params& p, int clusters, int threads, int smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(clusters * p.split));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  int most = resident[dev][p.split].load(std::memory_order_acquire);
-  if (!most) {
-    cfg.gridDim = dim3(p.split);
-    cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most < 1) {
-      cudaGetLastError();
-      return PQ2_ERR_CUDA;
-    }
-    resident[dev][p.split].store(most, std::memory_order_release);
-  }
-  // Equal shares: the clusters that run at once take as many tiles each.
-  const int each = (p.tiles + most - 1) / most;
-  const int clusters = (p.tiles + each - 1) / each;
-  const int cols = p.M * parts<XT>();
-  const int ring = warps * S::kStages * 2 * unit_bytes(GROUP, ZEROS);
-  const int red_tile = warps * cols * kPitch * 4, acc_tile = cols * kTileRows * 4;
-  const auto red = [&](int log) { return 2 * (red_tile << log); };
-  p.batch_log = 0;
-  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= 8 * 1024 &&
-         ring + red(p.batch_log + 1) + 4 * acc_tile <= S::kSmem)
-    ++p.batch_log;
-  p.block_tiles = std::min(each, (S::kSmem - ring - red(p.batch_log)) / acc_tile);
-  if (p.block_tiles < 1) return PQ2_ERR_SHAPE;
-
-  cfg.gridDim = dim3((unsigned)(clusters * p.split));
-  cfg.blockDim = dim3(warps * 32);
-  cfg.dynamicSmemBytes = ring + red(p.batch_log) + p.block_tiles * acc_tile;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
     cudaGetLastError();
@@ -673,35 +921,82 @@ int launch_one(W4Params p, int sms, cudaStream_t stream) {
   return PQ2_OK;
 }
 
-template <typename XT, int NT>
-int launch_nt(const W4Params& p, int group, bool zeros, int sms, cudaStream_t stream) {
-  switch (group * 2 + zeros) {
-    case 256: return launch_one<XT, NT, 128, false>(p, sms, stream);
-    case 257: return launch_one<XT, NT, 128, true>(p, sms, stream);
-    case 128: return launch_one<XT, NT, 64, false>(p, sms, stream);
-    case 129: return launch_one<XT, NT, 64, true>(p, sms, stream);
-    case 64: return launch_one<XT, NT, 32, false>(p, sms, stream);
-    default: return launch_one<XT, NT, 32, true>(p, sms, stream);
-  }
+template <typename XT, int GROUP, bool ZEROS>
+int launch_narrow(W4Params p, cudaStream_t stream) {
+  static std::atomic<int> known[64][9];
+  auto kern = w4_mmv_kernel<XT, 1, GROUP, ZEROS>;
+  int most = 0;
+  if (int st = resident_clusters(kern, known, p.split, kWarps * 32, kSmem, &most)) return st;
+  const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
+  const int warps = std::min(kWarps, pairs);
+  // Equal shares: the clusters that run at once take as many tiles each.
+  const int each = (p.tiles + most - 1) / most;
+  const int clusters = (p.tiles + each - 1) / each;
+  const int cols = p.M * parts<XT>();
+  const int ring = warps * kStages * 2 * unit_bytes(GROUP, ZEROS);
+  const int red_tile = warps * cols * kPitch * 4, acc_tile = cols * kTileRows * 4;
+  const auto red = [&](int log) { return 2 * (red_tile << log); };
+  p.batch_log = 0;
+  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= 8 * 1024 &&
+         ring + red(p.batch_log + 1) + 4 * acc_tile <= kSmem)
+    ++p.batch_log;
+  p.block_tiles = std::min(each, (kSmem - ring - red(p.batch_log)) / acc_tile);
+  if (p.block_tiles < 1) return PQ2_ERR_SHAPE;
+  return launch(kern, p, clusters, warps * 32,
+                ring + red(p.batch_log) + p.block_tiles * acc_tile, stream);
 }
 
-template <typename XT>
-int launch_x(W4Params p, int64_t M, int group, bool zeros, int sms, cudaStream_t stream) {
-  // At most 16 MMA columns at a time: 16 columns of x, or 8 of a 32-bit x.
-  constexpr int kMost = 16 / parts<XT>();
+template <typename XT, int NT, int GROUP, bool ZEROS>
+int launch_wide(const W4Params& p, cudaStream_t stream) {
+  static std::atomic<int> known[64][9];
+  auto kern = w4_wide_kernel<XT, NT, GROUP, ZEROS>;
+  constexpr int kThreads = (kWideWarps + kJoinWarps) * 32;
+  int most = 0;
+  if (int st = resident_clusters(kern, known, p.split, kThreads, kWideSmem, &most)) return st;
+  // Equal shares, of whole rounds' pairs of tiles.
+  const int each = (p.tiles + most - 1) / most;
+  const int clusters = (p.tiles + each - 1) / each;
+  const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
+  return launch(kern, p, clusters, kThreads, wide_smem<NT>(pairs, unit_bytes(GROUP, ZEROS)), stream);
+}
+
+template <typename XT, int GROUP, bool ZEROS>
+int launch_cols(W4Params p, int64_t M, cudaStream_t stream) {
+  // As many MMA columns at a time as the wide kernel's shared memory takes for
+  // this matrix (32, 24 or 16), else the narrow kernel's 8.
+  constexpr int kUnitB = unit_bytes(GROUP, ZEROS), kParts = parts<XT>();
+  const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
+  const int most = wide_smem<4>(pairs, kUnitB) <= kWideSmem   ? 32
+                   : wide_smem<3>(pairs, kUnitB) <= kWideSmem ? 24
+                   : wide_smem<2>(pairs, kUnitB) <= kWideSmem ? 16
+                                                              : 8;
   const int y_size = p.y_dtype == PQ2_F32 ? 4 : 2;
-  p.vector_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(XT) % 16 == 0;
-  for (int64_t m = 0; m < M; m += kMost) {
+  for (int64_t m = 0; m < M; m += most / kParts) {
     W4Params q = p;
-    q.M = (int)std::min<int64_t>(kMost, M - m);
+    q.M = (int)std::min<int64_t>(most / kParts, M - m);
     q.x = static_cast<const XT*>(p.x) + m * p.ldx;
     q.y = static_cast<uint8_t*>(p.y) + m * p.N * y_size;
-    int st;
-    st = q.M * parts<XT>() <= 8 ? launch_nt<XT, 1>(q, group, zeros, sms, stream)
-                                : launch_nt<XT, 2>(q, group, zeros, sms, stream);
+    const int cols = q.M * kParts;
+    const int st = cols <= 8    ? launch_narrow<XT, GROUP, ZEROS>(q, stream)
+                   : cols <= 16 ? launch_wide<XT, 2, GROUP, ZEROS>(q, stream)
+                   : cols <= 24 ? launch_wide<XT, 3, GROUP, ZEROS>(q, stream)
+                                : launch_wide<XT, 4, GROUP, ZEROS>(q, stream);
     if (st) return st;
   }
   return PQ2_OK;
+}
+
+template <typename XT>
+int launch_x(W4Params p, int64_t M, int group, bool zeros, cudaStream_t stream) {
+  p.vector_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx * sizeof(XT) % 16 == 0;
+  switch (group * 2 + zeros) {
+    case 256: return launch_cols<XT, 128, false>(p, M, stream);
+    case 257: return launch_cols<XT, 128, true>(p, M, stream);
+    case 128: return launch_cols<XT, 64, false>(p, M, stream);
+    case 129: return launch_cols<XT, 64, true>(p, M, stream);
+    case 64: return launch_cols<XT, 32, false>(p, M, stream);
+    default: return launch_cols<XT, 32, true>(p, M, stream);
+  }
 }
 
 }  // namespace
@@ -729,9 +1024,10 @@ int launch_w4_mmv(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t N,
   W4Params p{};
   p.x = x, p.plane = plane, p.y = y, p.ldx = ldx, p.N = N, p.K = (int)K, p.y_dtype = y_dtype;
   p.tiles = (int)tiles, p.units = (int)((K + kUnitK - 1) / kUnitK), p.overlap = overlap;
-  if (x_dtype == PQ2_BF16) return launch_x<__nv_bfloat16>(p, M, group, zeros, sm_count, stream);
-  if (x_dtype == PQ2_F16) return launch_x<__half>(p, M, group, zeros, sm_count, stream);
-  return launch_x<float>(p, M, group, zeros, sm_count, stream);
+  p.split = w4_split(p.tiles, p.units, sm_count);
+  if (x_dtype == PQ2_BF16) return launch_x<__nv_bfloat16>(p, M, group, zeros, stream);
+  if (x_dtype == PQ2_F16) return launch_x<__half>(p, M, group, zeros, stream);
+  return launch_x<float>(p, M, group, zeros, stream);
 }
 
 }  // namespace pq2
