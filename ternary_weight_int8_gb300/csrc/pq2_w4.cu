@@ -609,15 +609,15 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Par
 // The ranges of a cluster are joined round by round by warps of their own,
 // while the others are at the next round: a cluster barrier a round, two sets
 // of sums.  The order of the additions is the narrow kernel's.
-constexpr int kWideWarps = 8, kJoinWarps = 4, kWideStages = 4;
-constexpr int kRoundTiles = 2 * kWideWarps;
+constexpr int kTilesWarp = 1;  // TW
+constexpr int kRoundTiles = 16, kWideWarps = kRoundTiles / kTilesWarp, kJoinWarps = 4, kWideStages = 4;
 constexpr int kRoundRows = kRoundTiles * kTileRows;
 constexpr int kRoundPitch = kRoundRows + 4;  // floats per column: conflict-free
 constexpr int kWideSmem = 227 * 1024;
 
 template <int NT>
 constexpr int wide_smem(int pairs, int unit_b) {
-  return kWideWarps * kWideStages * 2 * unit_b + pairs * 8 * NT * 512 +
+  return kRoundTiles * kWideStages * unit_b + pairs * 8 * NT * 512 +
          (pairs + 2 * kRoundPitch) * 8 * NT * 4;
 }
 
@@ -639,30 +639,30 @@ __device__ __forceinline__ float remote_float(const float* p, int rank) {
 }
 
 // unit_product for two tiles, with the fragments from shared memory.
-template <int NT, int GROUP, bool ZEROS, bool ADD>
-__device__ __forceinline__ void unit_product2(const uint32_t (&unit)[2], int lane, uint32_t b_at,
-                                              float (&sum)[2][NT][4]) {
+template <int TW, int NT, int GROUP, bool ZEROS, bool ADD>
+__device__ __forceinline__ void unit_product2(const uint32_t (&unit)[TW], int lane, uint32_t b_at,
+                                              float (&sum)[TW][NT][4]) {
   constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
-  Side<GROUP, ZEROS> side[2];
-  side[0].load(unit[0], lane >> 2);
-  side[1].load(unit[1], lane >> 2);
-  uint4 c[2], b[NT];
+  Side<GROUP, ZEROS> side[TW];
+#pragma unroll
+  for (int h = 0; h < TW; ++h) side[h].load(unit[h], lane >> 2);
+  uint4 c[TW], b[NT];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    float d[2][NT][4];
+    float d[TW][NT][4];
 #pragma unroll
     for (int s2 = 0; s2 < kSteps; ++s2) {
       const int step = g * kSteps + s2;
       if (step % 4 == 0) {
-        c[0] = lds128(unit[0] + lane * 16 + step / 4 * 512);
-        c[1] = lds128(unit[1] + lane * 16 + step / 4 * 512);
+#pragma unroll
+        for (int h = 0; h < TW; ++h) c[h] = lds128(unit[h] + lane * 16 + step / 4 * 512);
       }
       if (step % 2 == 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) b[nt] = lds128(b_at + (step / 2 * NT + nt) * 512);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < TW; ++h) {
         const uint32_t w = step % 4 == 0 ? c[h].x : step % 4 == 1 ? c[h].y : step % 4 == 2 ? c[h].z : c[h].w;
         uint32_t a[4];
         decode(w, offset_of(side[h].low(g)).low, offset_of(side[h].high(g)).high, a);
@@ -676,7 +676,7 @@ __device__ __forceinline__ void unit_product2(const uint32_t (&unit)[2], int lan
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < TW; ++h) {
       const float2 s = side[h].scales(g);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
   constexpr int kParts = parts<XT>();
   constexpr bool kScaled = !std::is_same<XT, __half>::value;
   constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
-  constexpr int kCols = 8 * NT, kSlot = 2 * kUnitBytes;
+  constexpr int kCols = 8 * NT, TW = kTilesWarp, kSlot = TW * kUnitBytes;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane >> 2, t = lane & 3;
 
@@ -720,17 +720,18 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
 
   // The copies: items are (round, unit), both tiles of the warp's pair.
   const uint32_t ring = smem_u32(smem) + warp * (kWideStages * kSlot);
-  int ct = t0 + 2 * warp, cu = 0;  // tile and unit of the next copy
+  int ct = t0 + TW * warp, cu = 0;  // tile and unit of the next copy
   auto copy_next = [&](uint32_t slot) {
     if (ct < t1) {
       const uint8_t* src = p.plane + ct * tile_bytes + (int64_t)(u0 + cu) * kUnitBytes + lane * 16;
-      const bool both = ct + 1 < t1;
+      const bool both = TW == 2 && ct + 1 < t1;
       const uint32_t at = slot + lane * 16;
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
         cp_async16_if(lane < kChunks - 32 * j, at + 512 * j, src + 512 * j);
-        cp_async16_if(both && lane < kChunks - 32 * j, at + kUnitBytes + 512 * j,
-                      src + tile_bytes + 512 * j);
+        if (TW == 2)
+          cp_async16_if(both && lane < kChunks - 32 * j, at + kUnitBytes + 512 * j,
+                        src + tile_bytes + 512 * j);
       }
       if (++cu == units) {
         cu = 0;
@@ -768,11 +769,11 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
     const uint32_t ring_end = ring + kWideStages * kSlot;
     uint32_t cur = ring;
     for (int n = 0; n < rounds; ++n) {
-      const int tile = t0 + n * kRoundTiles + 2 * warp;
-      float acc[2][NT][4] = {};
+      const int tile = t0 + n * kRoundTiles + TW * warp;
+      float acc[TW][NT][4] = {};
       if (tile < t1) {
         const uint32_t second = tile + 1 < t1 ? kUnitBytes : 0;
-        float sum[2][NT][4];
+        float sum[TW][NT][4];
 #pragma unroll 1
         for (int q = 0; q < pairs; ++q) {
 #pragma unroll
@@ -784,18 +785,20 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
             dst = cur;
             cur += kSlot;
             cur = cur == ring_end ? ring : cur;
-            const uint32_t unit[2] = {dst, dst + second};
+            uint32_t unit[TW];
+#pragma unroll
+            for (int w = 0; w < TW; ++w) unit[w] = dst + w * second;
             const uint32_t b_at = smem_u32(frag) + (q * 8 + 4 * h) * NT * 512 + lane * 16;
             if (h == 0)
-              unit_product2<NT, GROUP, ZEROS, false>(unit, lane, b_at, sum);
+              unit_product2<TW, NT, GROUP, ZEROS, false>(unit, lane, b_at, sum);
             else
-              unit_product2<NT, GROUP, ZEROS, true>(unit, lane, b_at, sum);
+              unit_product2<TW, NT, GROUP, ZEROS, true>(unit, lane, b_at, sum);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 f = *reinterpret_cast<const float2*>(undo + q * kCols + 8 * nt + 2 * t);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < TW; ++h)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 acc[h][nt][e] = __fadd_rn(
@@ -804,11 +807,11 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
         }
       }
       if (n) cluster_wait();  // the sums of round n - 2 have been joined
-      float* s = sums + (n & 1) * kCols * kRoundPitch + 2 * t * kRoundPitch + 2 * warp * kTileRows + i;
+      float* s = sums + (n & 1) * kCols * kRoundPitch + 2 * t * kRoundPitch + TW * warp * kTileRows + i;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < TW; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             s[(8 * nt + e % 2) * kRoundPitch + h * kTileRows + e / 2 * 8] = acc[h][nt][e];
