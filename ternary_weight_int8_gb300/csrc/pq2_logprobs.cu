@@ -16,7 +16,8 @@
 // that; so a few of the warps' best threads give a limit, and only the threads
 // whose best reaches it (about 2 k of them) read that vector once more, or all
 // of theirs if the second reaches it too.  What reaches the limit there is
-// sorted.
+// sorted.  Logits of -inf stay out of this: a row with fewer than k others
+// takes its first ones at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -61,6 +62,7 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v);
   return v != v ? 1u : (b >> 31 ? ~b : b | 0x80000000u);
 }
+constexpr uint32_t kOrderOfMinusInf = 0x007FFFFFu;
 __device__ __forceinline__ float value_of(uint32_t order) {
   return order <= 1u ? -INFINITY
                      : __uint_as_float(order >> 31 ? order & 0x7FFFFFFFu : ~order);
@@ -357,6 +359,23 @@ __device__ __forceinline__ void merge_lists(Shared& s, int count, int warp, int 
   }
 }
 
+// Fills a list of n < k keys up to k with the row's first logits of -inf, then
+// NaN; one warp.
+template <typename XT>
+__device__ __noinline__ void fill_list(const XT* x, int64_t V, int n, int k, uint64_t* list) {
+  const int lane = threadIdx.x & 31;
+  for (int nan = 0; nan < 2; ++nan)
+    for (int64_t base = 0; base < V && n < k; base += 32) {
+      const float v = base + lane < V ? widen(x[base + lane]) : 0.f;
+      const bool take = nan ? v != v : v == -INFINITY;
+      const uint32_t who = __ballot_sync(0xffffffffu, take);
+      const int at = n + __popc(who & ((1u << lane) - 1));
+      if (take && at < k) list[at] = key_of(nan ? 1u : kOrderOfMinusInf, (uint32_t)(base + lane));
+      n += __popc(who);
+    }
+  __syncwarp();
+}
+
 template <typename XT, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobParams p) {
   constexpr int E = Vec<XT>::kElems;
@@ -446,15 +465,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
   part.join<32>(c2);
   if (lane == 0) s.sums[warp] = part;
   if (TOP) {
-    // This thread's best: its order (0: unknown, where a NaN or +inf may hide
-    // among its elements) and the indexes it may have.
+    // This thread's best: its order and the indexes it may have (0: nothing
+    // above -inf, or unknown, where a NaN or +inf may hide among its elements).
     const int count = v0 + tid < v1 ? (int)((v1 - v0 - tid + kThreads - 1) / kThreads) : 0;
     const int64_t best_v = v0 + tid + (int64_t)where * kThreads, first = head + best_v * E;
-    const uint32_t order = clean && count ? order_of(high) : 0;
+    const uint32_t order = clean && count && high > -INFINITY ? order_of(high) : 0;
     const uint64_t q = quota_th(order ? key_of(order, (uint32_t)(first + E - 1)) : 0, p.k);
     if (lane == 0) s.posted[warp] = q;
     __syncthreads();
-    const uint64_t limit = limit_of(p.k, s.posted);
+    const uint64_t limit = max64(limit_of(p.k, s.posted), (uint64_t)(kOrderOfMinusInf + 1) << 32);
     if (warp == 0) {
       const uint64_t key = single >= 0 ? key_of(order_of(single_x), (uint32_t)single) : 0;
       offer(best, key >= limit ? key : 0, p.k, s, warp, lane);
@@ -481,11 +500,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
         offer(best, key >= limit ? key : 0, p.k, s, warp, lane);
       }
     };
-    const bool hit = count && (!order || key_of(order, (uint32_t)first) >= limit);
+    const bool hit = count && (!clean || (order && key_of(order, (uint32_t)first) >= limit));
     // The first place where a vector other than the best can be.
     const int64_t other = head + (v0 + tid + (where ? 0 : kThreads)) * E;
     const bool whole =
-        hit && (!order || key_of(order_of(second), (uint32_t)other) >= limit);
+        hit && (!clean || key_of(order_of(second), (uint32_t)other) >= limit);
     // First the lanes that need one vector, then one whole thread after
     // another, 32 vectors at a time.
     uint32_t rest = __ballot_sync(0xffffffffu, whole);
@@ -576,6 +595,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
     }
     p.token_lp[row * p.T + j] = token < 0 ? 0.f : token >= p.V ? NAN : logprob(token_x);
   }
+  if (TOP && warp == 0) {
+    const int n = __popc(__ballot_sync(0xffffffffu, s.lists[0][lane] != 0));
+    if (n < p.k) fill_list(x, p.V, n, p.k, s.lists[0]);
+  }
   if (TOP && tid < p.k) {
     const uint64_t key = s.lists[0][tid];
     p.top_ids[row * p.k + tid] = 0xFFFFFFFFu - (uint32_t)key;
@@ -586,11 +609,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
 template <typename XT, bool TOP>
 int launch_one(LogprobParams p, int64_t M, int sms, cudaStream_t stream) {
   auto kern = logprobs_kernel<XT, TOP>;
-  // CTAs a row: enough to give every SM one, of at least 2048 elements each.
-  // (32 rows of 131072: 10.3 us in 256 CTAs, 14.6 us in 512; 300 rows of 100003:
-  // 21 us in 300 CTAs, 20 us in 600.)
+  // CTAs a row: enough to give every SM one, of at least 2048 elements each;
+  // two where that gives every SM two.  (32 rows of 131072: 10.3 us in 256 CTAs,
+  // 14.6 us in 512; 300 rows of 100003: 21 us in 300 CTAs, 20 us in 600.)
   p.split = 1;
-  while (p.split < kMaxCluster && M * p.split < sms && p.V / (2 * p.split) >= 2048)
+  while (p.split < kMaxCluster && M * p.split < (p.split == 1 ? 2 : 1) * sms &&
+         p.V / (2 * p.split) >= 2048)
     p.split *= 2;
   if (M * p.split > 0x7FFFFFFF) return PQ2_ERR_SHAPE;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
