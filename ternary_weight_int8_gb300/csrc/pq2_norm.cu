@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "pq2.h"
 #include "pq2_device.cuh"
@@ -100,46 +101,65 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
   return v;
 }
 
-// A thread's elements of a row: groups of E.  Vectors: group i is 16 bytes at
-// vector i * threads + tid (rows, K and pointers are multiples of 16 bytes).
-// Otherwise element e of group i is at (i * E + e) * threads + tid.
-template <typename T, bool VECTORS>
+// A thread's elements of a row: groups of E, each loaded as E / W pieces of W
+// elements (16 bytes where rows, K and pointers are multiples of that, else
+// the largest power of two that they are multiples of).  Piece c of group i is
+// at ((i * E / W + c) * threads + tid) * W.
+template <typename T, int W>
 struct Slice {
   using P = Pack<T>;
-  using Bits = typename P::Bits;
-  static constexpr int E = P::E;
+  static constexpr int E = P::E, kPieces = E / W, kBytes = W * (int)sizeof(T);
+  using Piece = typename std::conditional<
+      kBytes == 16, uint4,
+      typename std::conditional<kBytes == 8, uint2,
+                                typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::
+          type>::type;
+  // Where element e of group i is; a piece is in the row as a whole or not.
   static __device__ __forceinline__ int at(int i, int e) {
-    return VECTORS ? (i * (int)blockDim.x + (int)threadIdx.x) * E + e
-                   : (i * E + e) * (int)blockDim.x + (int)threadIdx.x;
+    return ((i * kPieces + e / W) * (int)blockDim.x + (int)threadIdx.x) * W + e % W;
   }
   // Group i; zeros beyond K.
   static __device__ __forceinline__ uint4 load(const T* row, int K, int i) {
-    if constexpr (VECTORS) {
+    if constexpr (kBytes == 16) {
       return at(i, 0) < K ? *reinterpret_cast<const uint4*>(row + at(i, 0)) : make_uint4(0, 0, 0, 0);
     } else {
-      const Bits* bits = reinterpret_cast<const Bits*>(row);
       uint32_t w[4] = {};
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (at(i, e) < K) w[e * 4 / E] |= (uint32_t)bits[at(i, e)] << (8 * e * sizeof(T) % 32);
+      for (int e = 0; e < E; e += W) {
+        if constexpr (kBytes == 8) {
+          const uint2 v = at(i, e) < K ? *reinterpret_cast<const uint2*>(row + at(i, e)) : make_uint2(0, 0);
+          w[e * 4 / E] = v.x, w[e * 4 / E + 1] = v.y;
+        } else {
+          if (at(i, e) < K)
+            w[e * 4 / E] |= (uint32_t) reinterpret_cast<const Piece*>(row)[at(i, e) / W]
+                            << (8 * e * sizeof(T) % 32);
+        }
+      }
       return make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   static __device__ __forceinline__ void store(T* row, int K, int i, uint4 v) {
-    if constexpr (VECTORS) {
+    if constexpr (kBytes == 16) {
       if (at(i, 0) < K) *reinterpret_cast<uint4*>(row + at(i, 0)) = v;
     } else {
-      Bits* bits = reinterpret_cast<Bits*>(row);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (at(i, e) < K) bits[at(i, e)] = (Bits)(w[e * 4 / E] >> (8 * e * sizeof(T) % 32));
+      for (int e = 0; e < E; e += W) {
+        if constexpr (kBytes == 8) {
+          if (at(i, e) < K)
+            *reinterpret_cast<uint2*>(row + at(i, e)) = make_uint2(w[e * 4 / E], w[e * 4 / E + 1]);
+        } else {
+          if (at(i, e) < K)
+            reinterpret_cast<Piece*>(row)[at(i, e) / W] =
+                (Piece)(w[e * 4 / E] >> (8 * e * sizeof(T) % 32));
+        }
+      }
     }
   }
 };
 
-// Threads of a CTA, at most.
-constexpr int threads_of(int v) { return v == 1 ? 256 : v == 2 ? 512 : 1024; }
+// Threads of a CTA, at most: small CTAs, so that several rows share an SM.
+constexpr int threads_of(int v) { return v > 2 ? 1024 : v == 1 ? 256 : 512; }
 
 // A thread's groups of a row, and of the weights.
 template <int V>
@@ -153,10 +173,10 @@ struct Weights {
 
 // One row in registers.  EARLY: the weights are in registers too, else they
 // are loaded group by group.
-template <typename T, int V, bool VECTORS, bool EARLY>
+template <typename T, int V, int W, bool EARLY>
 __device__ __forceinline__ void do_row(const NormParams& p, int64_t row, const Row<V>& in,
                                        const Weights<V>& w, float (*buf)[32]) {
-  using S = Slice<T, VECTORS>;
+  using S = Slice<T, W>;
   using P = Pack<T>;
   constexpr int E = P::E;
   const int K = (int)p.K;
@@ -196,7 +216,7 @@ __device__ __forceinline__ void do_row(const NormParams& p, int64_t row, const R
     // Places beyond K hold zeros, or what alpha makes of them.
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (S::at(i, VECTORS ? 0 : e) < K) s = fmaf(v[i][e], v[i][e], s);
+      if (S::at(i, e / W * W) < K) s = fmaf(v[i][e], v[i][e], s);
   }
   if (!p.n_out) return;
   inv = rsqrtf(fmaf(block_sum(s, buf[1]), p.one_over_k, p.eps));
@@ -217,10 +237,10 @@ __device__ __forceinline__ const T* gate_row(const NormParams& p, int64_t row) {
 }
 
 // A row a CTA.
-template <typename T, int V, bool VECTORS>
+template <typename T, int V, int W>
 __global__ void __launch_bounds__(threads_of(V), 1024 / threads_of(V)) norm_kernel(const NormParams p) {
-  using S = Slice<T, VECTORS>;
-  constexpr bool kEarly = VECTORS && V <= 2;
+  using S = Slice<T, W>;
+  constexpr bool kEarly = W == S::E && V <= 2;
   __shared__ float buf[2][32];
   const int K = (int)p.K;
   const int64_t row = blockIdx.x;
@@ -236,10 +256,10 @@ __global__ void __launch_bounds__(threads_of(V), 1024 / threads_of(V)) norm_kern
     if (kEarly && p.w_post) w.post[i] = S::load(static_cast<const T*>(p.w_post), K, i);
     if (kEarly && p.n_out) w.pre[i] = S::load(static_cast<const T*>(p.w_pre), K, i);
   }
-  do_row<T, V, VECTORS, kEarly>(p, row, in, w, buf);
+  do_row<T, V, W, kEarly>(p, row, in, w, buf);
 }
 
-template <typename T, int V, bool VECTORS>
+template <typename T, int V, int W>
 int launch_one(const NormParams& p, int threads, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)p.M);
@@ -250,35 +270,40 @@ int launch_one(const NormParams& p, int threads, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, norm_kernel<T, V, VECTORS>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, norm_kernel<T, V, W>, p) != cudaSuccess) {
     cudaGetLastError();
     return PQ2_ERR_LAUNCH;
   }
   return PQ2_OK;
 }
 
-template <typename T, bool VECTORS>
+template <typename T, int W>
 int launch_slices(const NormParams& p, cudaStream_t stream) {
   // Groups of 16 bytes a thread; eight are for fp32 rows beyond 16384 columns
   // alone.
   constexpr int E = 16 / sizeof(T);
   const int groups = (int)((p.K + E - 1) / E);
   const auto threads = [&](int v) { return ((groups + v - 1) / v + 31) / 32 * 32; };
-  if (threads(1) <= threads_of(1)) return launch_one<T, 1, VECTORS>(p, threads(1), stream);
-  if (threads(2) <= threads_of(2)) return launch_one<T, 2, VECTORS>(p, threads(2), stream);
+  if (threads(1) <= threads_of(1)) return launch_one<T, 1, W>(p, threads(1), stream);
+  if (threads(2) <= threads_of(2)) return launch_one<T, 2, W>(p, threads(2), stream);
   if (sizeof(T) == 2 || threads(4) <= threads_of(4))
-    return launch_one<T, 4, VECTORS>(p, threads(4), stream);
-  return launch_one<T, sizeof(T) == 4 ? 8 : 4, VECTORS>(p, threads(8), stream);
+    return launch_one<T, 4, W>(p, threads(4), stream);
+  return launch_one<T, sizeof(T) == 4 ? 8 : 4, W>(p, threads(8), stream);
 }
 
 template <typename T>
 int launch_type(const NormParams& p, cudaStream_t stream) {
-  const auto whole = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  const auto rows = [](int64_t ld) { return ld * sizeof(T) % 16 == 0; };
-  const bool vectors = whole(p.z) && whole(p.h) && whole(p.gate) && whole(p.w_post) &&
-                       whole(p.w_pre) && whole(p.h_out) && whole(p.n_out) && rows(p.K) &&
-                       rows(p.ldh) && (!p.z || rows(p.ldz)) && (!p.gate || rows(p.ldg));
-  return vectors ? launch_slices<T, true>(p, stream) : launch_slices<T, false>(p, stream);
+  // The lowest bit set in any address or row length, in bytes.
+  uint64_t bits = 16;
+  for (const void* q : {p.z, p.h, p.gate, p.w_post, p.w_pre, (const void*)p.h_out, (const void*)p.n_out})
+    bits |= reinterpret_cast<uintptr_t>(q);
+  bits |= (uint64_t)(p.K | p.ldh | (p.z ? p.ldz : 0) | (p.gate ? p.ldg : 0)) * sizeof(T);
+  switch (bits & -bits) {
+    case 16: return launch_slices<T, 16 / sizeof(T)>(p, stream);
+    case 8: return launch_slices<T, 8 / sizeof(T)>(p, stream);
+    case 4: return launch_slices<T, 4 / sizeof(T)>(p, stream);
+    default: return launch_slices<T, 1>(p, stream);
+  }
 }
 
 }  // namespace

@@ -164,12 +164,13 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
 }
 
 // What turns the two fields of a row into c - z: 1024 + z to subtract from
-// the low one, 64 + z (negated) to add to a sixteenth of the high one.
-struct Offset {
-  __half2 low, high;
-};
-__device__ __forceinline__ Offset offset_of(uint32_t z) {
-  return {half2_of((0x6400u + z) * 0x10001u), half2_of((0xD400u + 16 * z) * 0x10001u)};
+// the low one, -(64 + z) to add to a sixteenth of the high one.  As fp16 their
+// high bytes are 0x64 and 0xD4, their low bytes z and 16 z.
+__device__ __forceinline__ __half2 offset_low(uint32_t zeros, int g) {
+  return half2_of(__byte_perm(zeros, 0x64u, 0x4040u + 0x0101u * g));
+}
+__device__ __forceinline__ __half2 offset_high(uint32_t zeros16, int g) {
+  return half2_of(__byte_perm(zeros16, 0xD4u, 0x4040u + 0x0101u * g));
 }
 
 // (v & mask) | 0x64006400 in one operation.
@@ -331,8 +332,12 @@ struct Side {
     }
   }
   __device__ __forceinline__ float2 scales(int g) const { return __half22float2(half2_of(scale[g])); }
-  __device__ __forceinline__ uint32_t low(int g) const { return ZEROS ? zero >> 8 * g & 15 : 8; }
-  __device__ __forceinline__ uint32_t high(int g) const { return ZEROS ? zero >> (8 * g + 4) & 15 : 8; }
+  __device__ __forceinline__ __half2 low(int g) const {
+    return ZEROS ? offset_low(zero & 0x0F0F0F0Fu, g) : half2_of(0x64086408u);
+  }
+  __device__ __forceinline__ __half2 high(int g) const {
+    return ZEROS ? offset_high(zero & 0xF0F0F0F0u, g) : half2_of(0xD480D480u);
+  }
 };
 
 // One unit's products with the columns b[nt][j], scaled by the groups' scales:
@@ -347,7 +352,7 @@ __device__ __forceinline__ void unit_product(uint32_t unit, int lane, const uint
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     const float2 s = side.scales(g);
-    const Offset o0 = offset_of(side.low(g)), o1 = offset_of(side.high(g));
+    const __half2 low = side.low(g), high = side.high(g);
     float d[NT][4];
 #pragma unroll
     for (int s2 = 0; s2 < kSteps; ++s2) {
@@ -355,7 +360,7 @@ __device__ __forceinline__ void unit_product(uint32_t unit, int lane, const uint
       if (step % 4 == 0) c = lds128(unit + lane * 16 + step / 4 * 512);
       const uint32_t w = step % 4 == 0 ? c.x : step % 4 == 1 ? c.y : step % 4 == 2 ? c.z : c.w;
       uint32_t a[4];
-      decode(w, o0.low, o1.high, a);
+      decode(w, low, high, a);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 bb = b[nt][j0 + step / 2];
@@ -627,15 +632,18 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float remote_float(const float* p, int rank) {
-  float v;
+__device__ __forceinline__ float4 remote_float4(const float* p, int rank) {
+  float4 v;
   asm volatile(
-      "{\n\t.reg .u32 at;\n\tmapa.shared::cluster.u32 at, %1, %2;\n\t"
-      "ld.shared::cluster.f32 %0, [at];\n\t}"
-      : "=f"(v)
+      "{\n\t.reg .u32 at;\n\tmapa.shared::cluster.u32 at, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [at];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
       : "r"(smem_u32(p)), "r"(rank)
       : "memory");
   return v;
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 // unit_product for two tiles, with the fragments from shared memory.
@@ -665,7 +673,7 @@ __device__ __forceinline__ void unit_product2(const uint32_t (&unit)[TW], int la
       for (int h = 0; h < TW; ++h) {
         const uint32_t w = step % 4 == 0 ? c[h].x : step % 4 == 1 ? c[h].y : step % 4 == 2 ? c[h].z : c[h].w;
         uint32_t a[4];
-        decode(w, offset_of(side[h].low(g)).low, offset_of(side[h].high(g)).high, a);
+        decode(w, side[h].low(g), side[h].high(g), a);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if (s2 == 0)
@@ -827,28 +835,28 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
       const int64_t n0 = (int64_t)(t0 + n * kRoundTiles) * kTileRows;
       const int rows = min(kRoundTiles, t1 - t0 - n * kRoundTiles) * kTileRows;
       const float* s = sums + (n & 1) * kCols * kRoundPitch;
-      for (int e = threadIdx.x - kWideWarps * 32 + rank * kJoinWarps * 32; e < kRoundRows * p.M;
+      // Four rows of a column a thread.
+      for (int e = threadIdx.x - kWideWarps * 32 + rank * kJoinWarps * 32; e < kRoundRows / 4 * p.M;
            e += p.split * kJoinWarps * 32) {
-        const int m = e / kRoundRows, r = e % kRoundRows;
+        const int m = e / (kRoundRows / 4), r = e % (kRoundRows / 4) * 4;
         if (r >= rows || n0 + r >= p.N) continue;
-        float v[8][kParts];
+        float4 v[8][kParts];
 #pragma unroll
         for (int z = 0; z < 8; ++z)
           if (z < p.split) {
 #pragma unroll
             for (int q = 0; q < kParts; ++q)
-              v[z][q] = remote_float(s + (m * kParts + q) * kRoundPitch + r, z);
+              v[z][q] = remote_float4(s + (m * kParts + q) * kRoundPitch + r, z);
           }
-        float y = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int z = 0; z < 8; ++z)
-          if (z < p.split) {
-            float sum = 0.f;
+          if (z < p.split) y = add4(y, kParts == 2 ? add4(v[z][kParts - 1], v[z][0]) : v[z][0]);
+        const int64_t at = m * p.N + n0 + r;
+        const float out[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int q = kParts - 1; q >= 0; --q) sum += v[z][q];
-            y += sum;
-          }
-        store_y(p.y, p.y_dtype, m * p.N + n0 + r, y);
+        for (int h = 0; h < 4; ++h)
+          if (n0 + r + h < p.N) store_y(p.y, p.y_dtype, at + h, out[h]);
       }
     }
   }
