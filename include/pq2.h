@@ -562,8 +562,8 @@ int pq2_w4_prepare(const uint8_t *codes, int64_t ldc, const uint16_t *scales,
                    uint8_t *plane, void *stream);
 
 /* pq2_w4_mmv — y = x W^T for M = 1..32.  c - z is exact, x is taken in fp16:
- * an fp16 x as it is; a bf16 x scaled by a power of two per 128 columns
- * (exact down to 2^-28 of the largest |x| among them, within 2^-39 of it
+ * an fp16 x as it is; a bf16 x scaled by a power of two per 256 columns at
+ * most (exact down to 2^-28 of the largest |x| among them, within 2^-39 of it
  * below); a 32-bit x as the sum of two such parts (within 2^-24 of its
  * value).  Products are exact, sums and y fp32.
  *   x        (device, or pinned host memory as for pq2_mmv) x_dtype

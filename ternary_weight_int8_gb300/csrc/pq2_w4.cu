@@ -133,8 +133,8 @@ struct W4Params {
 // field would need a shift of its own, 7 instead of 5 integer operations per
 // 8 weights, and integer operations run at half rate.)
 //
-// A bf16 or 32-bit x is scaled by a power of two, one per column and unit, so
-// that the unit's largest |x| lies in [2^14, 2^15).  A bf16 value is then
+// A bf16 or 32-bit x is scaled by a power of two, one per column and pair of
+// units, so that the pair's largest |x| lies in [2^14, 2^15).  A bf16 value is then
 // exact in fp16 down to 2^-28 of that largest one, and 2^-39 of it is the most
 // that rounding below costs.  A 32-bit x is the sum of two fp16 parts (within
 // 2^-24 of its value), each an MMA column of its own.

@@ -495,12 +495,19 @@ def pq2_linear_grouped(x, codes, scales, act_group: int, y=None, out_dtype=torch
     return y
 
 
+def _on_device(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda and not t.is_pinned():
+            raise ValueError("Expected CUDA tensors (or pinned host memory)")
+
+
 def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stream=None):
     """4-bit codes u8[N][K/2] (column 2j in the low half of byte j), fp16
     scales [N][K/group] and zero points u8[N][K/group] (None: 8) -> the plane
     u8 that pq2_w4_mmv streams."""
     if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.stride(1) != 1:
         raise ValueError("codes must be a 2-D uint8 tensor with unit column stride")
+    _on_device(codes, scales, zeros, plane)
     N, K = codes.shape[0], 2 * codes.shape[1]
     for t, dt, what in ((scales, torch.float16, "fp16 scales"), (zeros, torch.uint8, "uint8 zeros")):
         if t is not None and (t.dtype != dt or t.shape != (N, K // group)
@@ -534,6 +541,7 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     else:
         _check_out(y, (M, N))
+    _on_device(x, plane, y)
     key = (N, K, group, zeros)
     if key not in _w4_bytes:
         _w4_bytes[key] = lib().pq2_w4_plane_bytes(N, K, group, int(zeros))
@@ -556,6 +564,7 @@ def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entr
     if tokens is not None and (tokens.dtype != torch.int64 or not tokens.is_contiguous()
                                or tokens.shape[0] != M):
         raise ValueError("Expected contiguous int64 tokens with a row per row of logits")
+    _on_device(logits, tokens)
     T = 0 if tokens is None or not M else tokens.numel() // M
     if out is None:
         dev = logits.device
@@ -564,6 +573,7 @@ def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entr
                torch.empty((M, k), dtype=torch.int64, device=dev),
                torch.empty((M, k), dtype=torch.float32, device=dev))
     else:
+        _on_device(*out)
         _check_out(out[0], (M, T), torch.float32)
         if out[1] is not None:
             _check_out(out[1], (M,), torch.float32)
@@ -601,6 +611,7 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
     for w in (w_pre, w_post):
         if w is not None and (w.numel() != K or w.dtype != dtype or not w.is_contiguous()):
             raise ValueError("the norm weights must be contiguous [K] of h's type")
+    _on_device(z, h, w_pre, w_post, gate, h_out, n_out)
     if h_out is not None:
         _check_out(h_out, shape, dtype)
     elif z is not None:

@@ -106,6 +106,37 @@ def test_within_bound(M, N, K, G, zeros, dtype):
         check(y, x, w)
 
 
+@pytest.mark.parametrize("M", [3, 13, 32])
+@pytest.mark.parametrize("N,K,G", [(100, 70016, 64), (64, 30720, 128), (3000, 17408, 32)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_long_rows(M, N, K, G, dtype):
+    """Ranges of units too long for one pass, or for the wide kernel's shared
+    memory."""
+    codes, scales, z = raw(N, K, G, True, seed=N)
+    plane = pq2.pq2_w4_prepare(codes, scales, z, group=G)
+    x = acts(M, K, dtype, seed=M)
+    y = pq2.pq2_w4_mmv(x, plane, N, G, zeros=True)
+    check(y, x, dense(codes, scales, z, G))
+    assert torch.equal(pq2.pq2_w4_mmv(x[:1], plane, N, G, zeros=True), y[:1])
+
+
+def test_small_and_large_x():
+    """Magnitudes far from one keep their precision: tiny, huge and mixed
+    columns of x."""
+    N, K, G = 50, 768, 64
+    codes, scales, z = raw(N, K, G, False, seed=15)
+    plane = pq2.pq2_w4_prepare(codes, scales, group=G)
+    for dtype in (BF16, F32):
+        x = acts(6, K, F32, seed=16)
+        x[0] *= 1e-30
+        x[1] *= 1e30
+        x[2, ::2] *= 1e-6
+        x[3, 256:512] *= 1e20
+        x[4, :256] *= 1e-20
+        x = x.to(dtype)
+        check(pq2.pq2_w4_mmv(x, plane, N, G), x, dense(codes, scales, None, G))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("pad,shift", [(8, 0), (1, 0), (3, 1), (0, 1), (32, 4)])
 def test_strides_and_alignments_of_x(dtype, pad, shift):
@@ -229,7 +260,11 @@ def test_refusals():
                 lambda: pq2.pq2_w4_mmv(torch.zeros((0, K), device="cuda"), plane, N, G)):
         with pytest.raises(pq2.Pq2Error):
             bad()
-    with pytest.raises(ValueError):
-        pq2.pq2_w4_prepare(codes, scales, z, group=128)
+    for bad in (lambda: pq2.pq2_w4_prepare(codes, scales, z, group=128),
+                lambda: pq2.pq2_w4_mmv(torch.zeros((1, K)), plane, N, G, zeros=True),
+                lambda: pq2.pq2_w4_mmv(torch.zeros((2, K), device="cuda"), plane, N, G, zeros=True,
+                                       y=torch.empty((1, N), device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
     with pytest.raises(ValueError):
         pq2.pq2_w4_prepare(codes.t(), scales, z, group=G)
