@@ -16,7 +16,9 @@
 // that; so a few of the warps' best threads give a limit, and only the threads
 // whose best reaches it (about 2 k of them) read that vector once more, or all
 // of theirs if the second reaches it too.  What reaches the limit there is
-// sorted.  Logits of -inf stay out of this: a row with fewer than k others
+// sorted.  (2048 rows of 131072 bf16: 83 us without alternatives, 92 us with
+// one, 99 us with 20; 0.96 .. 0.80 of the measured copy rate.  Lists kept during
+// the pass cost 122 us.)  Logits of -inf stay out of this: a row with fewer than k others
 // takes its first ones at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

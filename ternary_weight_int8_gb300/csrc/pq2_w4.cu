@@ -109,6 +109,9 @@ __global__ void w4_prepare_kernel(W4PrepParams p) {
 // a private ring of cp.async copies, so a weight byte is read once and x once
 // per CTA.  The warps' scaled sums of a tile meet in shared memory, where they
 // are added in the order of the pairs.
+// Bound by instruction issue (133 a unit, 72 of them the decoding) just above
+// its bytes: 131072 x 5120 at M = 1 in 62 us, 0.85 of the measured copy rate
+// (75 us with one unit a warp; 65 us with five CTAs an SM at 96 registers).
 // The order of a y's additions: MMA steps of a group, groups of a unit, the
 // two units of a pair, pairs of a CTA's range in ascending order, ranges in
 // cluster order.
@@ -340,43 +343,44 @@ struct Side {
   }
 };
 
-// One unit's products with the columns b[nt][j], scaled by the groups' scales:
-// sum = ADD ? sum + unit : unit.
-template <int NT, int GROUP, bool ZEROS, bool ADD, int BJ>
-__device__ __forceinline__ void unit_product(uint32_t unit, int lane, const uint4 (&b)[NT][BJ], int j0,
-                                             float (&sum)[NT][4]) {
+__device__ __forceinline__ uint32_t word_of(uint4 c, int i) {
+  return i == 0 ? c.x : i == 1 ? c.y : i == 2 ? c.z : c.w;
+}
+// sum = (ADD or not the unit's first group ? sum : 0) + s d; s of rows i, i + 8.
+template <bool ADD>
+__device__ __forceinline__ void add_scaled(int g, float2 s, const float* d, float* sum) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float sc = e < 2 ? s.x : s.y;
+    sum[e] = g == 0 && !ADD ? __fmul_rn(sc, d[e]) : __fmaf_rn(sc, d[e], sum[e]);
+  }
+}
+
+// One unit's products with 8 columns (fragments b), scaled by the groups'
+// scales: sum = ADD ? sum + unit : unit.
+template <int GROUP, bool ZEROS, bool ADD>
+__device__ __forceinline__ void unit_product(uint32_t unit, int lane, const uint4* b, float* sum) {
   constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
   Side<GROUP, ZEROS> side;
   side.load(unit, lane >> 2);
   uint4 c;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    const float2 s = side.scales(g);
     const __half2 low = side.low(g), high = side.high(g);
-    float d[NT][4];
+    float d[4];
 #pragma unroll
     for (int s2 = 0; s2 < kSteps; ++s2) {
       const int step = g * kSteps + s2;
       if (step % 4 == 0) c = lds128(unit + lane * 16 + step / 4 * 512);
-      const uint32_t w = step % 4 == 0 ? c.x : step % 4 == 1 ? c.y : step % 4 == 2 ? c.z : c.w;
       uint32_t a[4];
-      decode(w, low, high, a);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4 bb = b[nt][j0 + step / 2];
-        if (s2 == 0)
-          mma16816<true>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
-        else
-          mma16816<false>(d[nt], a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
-      }
+      decode(word_of(c, step % 4), low, high, a);
+      const uint4 bb = b[step / 2];
+      if (s2 == 0)
+        mma16816<true>(d, a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
+      else
+        mma16816<false>(d, a, step % 2 ? bb.z : bb.x, step % 2 ? bb.w : bb.y);
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float sc = e < 2 ? s.x : s.y;
-        sum[nt][e] = g == 0 && !ADD ? __fmul_rn(sc, d[nt][e]) : __fmaf_rn(sc, d[nt][e], sum[nt][e]);
-      }
+    add_scaled<ADD>(g, side.scales(g), d, sum);
   }
 }
 
@@ -402,7 +406,7 @@ __device__ __forceinline__ void dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <typename XT, int NT, int GROUP, bool ZEROS>
+template <typename XT, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Params p) {
   constexpr int kParts = parts<XT>();
   constexpr bool kScaled = !std::is_same<XT, __half>::value;
@@ -469,8 +473,8 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Par
   // dst: the slot that the item before the current one used; cur: its own.
   uint32_t cur = ring;
   const uint32_t out0 = smem_u32(red + warp * red_warp + 2 * t * kPitch + i);
-  uint4 b[NT][8];
-  float undo[NT][2];
+  uint4 b[8];
+  float undo[2];
   int buf = 0;
   bool waited = p.overlap != 2;
   for (int b0 = t0; b0 < t1; b0 += p.block_tiles) {
@@ -482,25 +486,20 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Par
       if (!idle && (b0 == t0 || pairs > warps)) {
         // A unit beyond the range belongs to another CTA.
         const int64_t end = min((int64_t)p.K, (int64_t)u1 * kUnitK);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int v = 8 * nt + i, m = v / kParts;
-          const XT* x = m < p.M ? static_cast<const XT*>(p.x) + m * p.ldx : nullptr;
-          const float f = load_b(x, (int64_t)(u0 + 2 * pair) * kUnitK + 8 * t, end, v % kParts,
-                                 p.vector_x != 0, b[nt]);
-          if (kScaled) {
-            undo[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-            undo[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-          }
+        const int m = i / kParts;
+        const XT* x = m < p.M ? static_cast<const XT*>(p.x) + m * p.ldx : nullptr;
+        const float f = load_b(x, (int64_t)(u0 + 2 * pair) * kUnitK + 8 * t, end, i % kParts,
+                               p.vector_x != 0, b);
+        if (kScaled) {
+          undo[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+          undo[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
         }
       }
       // The fragments are values of their own from here on, not to be formed
       // again from x inside the loop.
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          asm volatile("" : "+r"(b[nt][j].x), "+r"(b[nt][j].y), "+r"(b[nt][j].z), "+r"(b[nt][j].w));
+      for (int j = 0; j < 8; ++j)
+        asm volatile("" : "+r"(b[j].x), "+r"(b[j].y), "+r"(b[j].z), "+r"(b[j].w));
       for (int tb = b0; tb < b1; tb += 1 << p.batch_log) {
         const int te = min(tb + (1 << p.batch_log), b1);
         uint32_t out = out0 + buf * red_buf * 4;
@@ -519,22 +518,18 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Par
             dst = cur;
             cur += kSlot;
             cur = cur == ring_end ? ring : cur;
-            float sum[NT][4];
+            float sum[4];
             if (two) {
-              unit_product<NT, GROUP, ZEROS, false>(dst, lane, b, 0, sum);
-              unit_product<NT, GROUP, ZEROS, true>(dst + kUnitBytes, lane, b, 4, sum);
+              unit_product<GROUP, ZEROS, false>(dst, lane, b, sum);
+              unit_product<GROUP, ZEROS, true>(dst + kUnitBytes, lane, b + 4, sum);
             } else {
-              unit_product<NT, GROUP, ZEROS, false>(dst, lane, b, 0, sum);
+              unit_product<GROUP, ZEROS, false>(dst, lane, b, sum);
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t at = out + (8 * nt + h) * kPitch * 4;
-                const bool on = 8 * nt + 2 * t + h < cols;
-                sts_if(on, at, kScaled ? __fmul_rn(sum[nt][h], undo[nt][h]) : sum[nt][h]);
-                sts_if(on, at + 32, kScaled ? __fmul_rn(sum[nt][h + 2], undo[nt][h]) : sum[nt][h + 2]);
-              }
+            for (int e = 0; e < 4; ++e) {
+              const float v = kScaled ? __fmul_rn(sum[e], undo[e % 2]) : sum[e];
+              sts_if(2 * t + e % 2 < cols, out + (e % 2 * kPitch + e / 2 * 8) * 4, v);
+            }
             out += red_tile * 4;
           }
         }
@@ -609,13 +604,16 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Par
 
 // The wide kernel, for 9 to 32 columns.  x fragments of that many columns do
 // not fit a warp's registers, so a CTA keeps those of its range of units in
-// shared memory, and a warp takes two tiles through the whole range: each
-// fragment it loads serves both, and its sums need no join within the CTA.
+// shared memory, and a warp takes a tile through the whole range: its sums need
+// no join within the CTA.
 // The ranges of a cluster are joined round by round by warps of their own,
 // while the others are at the next round: a cluster barrier a round, two sets
 // of sums.  The order of the additions is the narrow kernel's.
-constexpr int kTilesWarp = 1;  // TW
-constexpr int kRoundTiles = 16, kWideWarps = kRoundTiles / kTilesWarp, kJoinWarps = 4, kWideStages = 4;
+// Bound by mma.sync with fp32 accumulation, about 550 multiply-adds a clock and
+// SM: 131072 x 5120 at M = 32 in 140 us (297 us with 16 columns a launch in the
+// narrow form, 145 us with 8 warps of two tiles).
+constexpr int kWideWarps = 16, kJoinWarps = 4, kWideStages = 4;
+constexpr int kRoundTiles = kWideWarps;
 constexpr int kRoundRows = kRoundTiles * kTileRows;
 constexpr int kRoundPitch = kRoundRows + 4;  // floats per column: conflict-free
 constexpr int kWideSmem = 227 * 1024;
@@ -646,55 +644,39 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// unit_product for two tiles, with the fragments from shared memory.
-template <int TW, int NT, int GROUP, bool ZEROS, bool ADD>
-__device__ __forceinline__ void unit_product2(const uint32_t (&unit)[TW], int lane, uint32_t b_at,
-                                              float (&sum)[TW][NT][4]) {
+// unit_product for NT column tiles, with the fragments from shared memory.
+template <int NT, int GROUP, bool ZEROS, bool ADD>
+__device__ __forceinline__ void unit_product_wide(uint32_t unit, int lane, uint32_t b_at,
+                                                  float (&sum)[NT][4]) {
   constexpr int kGroups = kUnitK / GROUP, kSteps = GROUP / 16;
-  Side<GROUP, ZEROS> side[TW];
-#pragma unroll
-  for (int h = 0; h < TW; ++h) side[h].load(unit[h], lane >> 2);
-  uint4 c[TW], b[NT];
+  Side<GROUP, ZEROS> side;
+  side.load(unit, lane >> 2);
+  uint4 c, b[NT];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    float d[TW][NT][4];
+    const __half2 low = side.low(g), high = side.high(g);
+    float d[NT][4];
 #pragma unroll
     for (int s2 = 0; s2 < kSteps; ++s2) {
       const int step = g * kSteps + s2;
-      if (step % 4 == 0) {
-#pragma unroll
-        for (int h = 0; h < TW; ++h) c[h] = lds128(unit[h] + lane * 16 + step / 4 * 512);
-      }
+      if (step % 4 == 0) c = lds128(unit + lane * 16 + step / 4 * 512);
       if (step % 2 == 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) b[nt] = lds128(b_at + (step / 2 * NT + nt) * 512);
       }
+      uint32_t a[4];
+      decode(word_of(c, step % 4), low, high, a);
 #pragma unroll
-      for (int h = 0; h < TW; ++h) {
-        const uint32_t w = step % 4 == 0 ? c[h].x : step % 4 == 1 ? c[h].y : step % 4 == 2 ? c[h].z : c[h].w;
-        uint32_t a[4];
-        decode(w, side[h].low(g), side[h].high(g), a);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (s2 == 0)
-            mma16816<true>(d[h][nt], a, step % 2 ? b[nt].z : b[nt].x, step % 2 ? b[nt].w : b[nt].y);
-          else
-            mma16816<false>(d[h][nt], a, step % 2 ? b[nt].z : b[nt].x, step % 2 ? b[nt].w : b[nt].y);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        if (s2 == 0)
+          mma16816<true>(d[nt], a, step % 2 ? b[nt].z : b[nt].x, step % 2 ? b[nt].w : b[nt].y);
+        else
+          mma16816<false>(d[nt], a, step % 2 ? b[nt].z : b[nt].x, step % 2 ? b[nt].w : b[nt].y);
       }
     }
+    const float2 s = side.scales(g);
 #pragma unroll
-    for (int h = 0; h < TW; ++h) {
-      const float2 s = side[h].scales(g);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float sc = e < 2 ? s.x : s.y;
-          sum[h][nt][e] = g == 0 && !ADD ? __fmul_rn(sc, d[h][nt][e])
-                                         : __fmaf_rn(sc, d[h][nt][e], sum[h][nt][e]);
-        }
-    }
+    for (int nt = 0; nt < NT; ++nt) add_scaled<ADD>(g, s, d[nt], sum[nt]);
   }
 }
 
@@ -703,7 +685,7 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
   constexpr int kParts = parts<XT>();
   constexpr bool kScaled = !std::is_same<XT, __half>::value;
   constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
-  constexpr int kCols = 8 * NT, TW = kTilesWarp, kSlot = TW * kUnitBytes;
+  constexpr int kCols = 8 * NT, kSlot = kUnitBytes;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane >> 2, t = lane & 3;
 
@@ -726,20 +708,16 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!p.overlap) dependency_wait();
 
-  // The copies: items are (round, unit), both tiles of the warp's pair.
+  // The copies: items are (round, unit) of the warp's tile.
   const uint32_t ring = smem_u32(smem) + warp * (kWideStages * kSlot);
-  int ct = t0 + TW * warp, cu = 0;  // tile and unit of the next copy
+  int ct = t0 + warp, cu = 0;  // tile and unit of the next copy
   auto copy_next = [&](uint32_t slot) {
     if (ct < t1) {
       const uint8_t* src = p.plane + ct * tile_bytes + (int64_t)(u0 + cu) * kUnitBytes + lane * 16;
-      const bool both = TW == 2 && ct + 1 < t1;
       const uint32_t at = slot + lane * 16;
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
         cp_async16_if(lane < kChunks - 32 * j, at + 512 * j, src + 512 * j);
-        if (TW == 2)
-          cp_async16_if(both && lane < kChunks - 32 * j, at + kUnitBytes + 512 * j,
-                        src + tile_bytes + 512 * j);
       }
       if (++cu == units) {
         cu = 0;
@@ -777,13 +755,12 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
     const uint32_t ring_end = ring + kWideStages * kSlot;
     uint32_t cur = ring;
     for (int n = 0; n < rounds; ++n) {
-      const int tile = t0 + n * kRoundTiles + TW * warp;
-      float acc[TW][NT][4] = {};
-      if (tile < t1) {
-        const uint32_t second = tile + 1 < t1 ? kUnitBytes : 0;
-        float sum[TW][NT][4];
+      float acc[NT][4] = {};
+      if (t0 + n * kRoundTiles + warp < t1) {
+        float sum[NT][4];
 #pragma unroll 1
         for (int q = 0; q < pairs; ++q) {
+          const uint32_t b_at = smem_u32(frag) + q * 8 * NT * 512 + lane * 16;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (2 * q + h >= units) break;
@@ -793,36 +770,27 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
             dst = cur;
             cur += kSlot;
             cur = cur == ring_end ? ring : cur;
-            uint32_t unit[TW];
-#pragma unroll
-            for (int w = 0; w < TW; ++w) unit[w] = dst + w * second;
-            const uint32_t b_at = smem_u32(frag) + (q * 8 + 4 * h) * NT * 512 + lane * 16;
             if (h == 0)
-              unit_product2<TW, NT, GROUP, ZEROS, false>(unit, lane, b_at, sum);
+              unit_product_wide<NT, GROUP, ZEROS, false>(dst, lane, b_at, sum);
             else
-              unit_product2<TW, NT, GROUP, ZEROS, true>(unit, lane, b_at, sum);
+              unit_product_wide<NT, GROUP, ZEROS, true>(dst, lane, b_at + 4 * NT * 512, sum);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 f = *reinterpret_cast<const float2*>(undo + q * kCols + 8 * nt + 2 * t);
 #pragma unroll
-            for (int h = 0; h < TW; ++h)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[h][nt][e] = __fadd_rn(
-                    acc[h][nt][e], kScaled ? __fmul_rn(sum[h][nt][e], e % 2 ? f.y : f.x) : sum[h][nt][e]);
+            for (int e = 0; e < 4; ++e)
+              acc[nt][e] = __fadd_rn(
+                  acc[nt][e], kScaled ? __fmul_rn(sum[nt][e], e % 2 ? f.y : f.x) : sum[nt][e]);
           }
         }
       }
       if (n) cluster_wait();  // the sums of round n - 2 have been joined
-      float* s = sums + (n & 1) * kCols * kRoundPitch + 2 * t * kRoundPitch + TW * warp * kTileRows + i;
+      float* s = sums + (n & 1) * kCols * kRoundPitch + 2 * t * kRoundPitch + warp * kTileRows + i;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < TW; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[(8 * nt + e % 2) * kRoundPitch + h * kTileRows + e / 2 * 8] = acc[h][nt][e];
+        for (int e = 0; e < 4; ++e) s[(8 * nt + e % 2) * kRoundPitch + e / 2 * 8] = acc[nt][e];
       cluster_arrive();
     }
     if (rounds) cluster_wait();
@@ -935,7 +903,7 @@ int launch(Kernel kern, const W4Params& p, int clusters, int threads, int smem, 
 template <typename XT, int GROUP, bool ZEROS>
 int launch_narrow(W4Params p, cudaStream_t stream) {
   static std::atomic<int> known[64][9];
-  auto kern = w4_mmv_kernel<XT, 1, GROUP, ZEROS>;
+  auto kern = w4_mmv_kernel<XT, GROUP, ZEROS>;
   int most = 0;
   if (int st = resident_clusters(kern, known, p.split, kWarps * 32, kSmem, &most)) return st;
   const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
