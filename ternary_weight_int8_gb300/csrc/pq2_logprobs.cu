@@ -398,6 +398,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  // The row's first vectors are on their way before anything is waited for.
+  uint4 next[kUnroll];
+  auto load = [&](int64_t base) {
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int64_t v = base + j * kThreads + tid;
+      next[j] = v < v1 ? body[v]
+                       : make_uint4(Vec<XT>::kNone, Vec<XT>::kNone, Vec<XT>::kNone, Vec<XT>::kNone);
+    }
+  };
+  load(v0);
+
   Running sums{-3.402823466e38f, 0, 0};
   Best best{};
 
@@ -422,16 +434,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobPara
     sums.add(single_x, -INFINITY, c2);
   }
 
-  uint4 next[kUnroll];
-  auto load = [&](int64_t base) {
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int64_t v = base + j * kThreads + tid;
-      next[j] = v < v1 ? body[v]
-                       : make_uint4(Vec<XT>::kNone, Vec<XT>::kNone, Vec<XT>::kNone, Vec<XT>::kNone);
-    }
-  };
-  load(v0);
   float high = -INFINITY, second = -INFINITY;  // largest vector maxima
   int where = 0, at = 0;                       // the vector of `high`
   for (int64_t base = v0; base < v1; base += kUnroll * kThreads) {
