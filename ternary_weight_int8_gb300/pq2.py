@@ -513,9 +513,11 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
         if t is not None and (t.dtype != dt or t.shape != (N, K // group)
                               or not t.is_contiguous()):
             raise ValueError(f"Expected contiguous {what} of shape [N][K / group]")
+    nbytes = lib().pq2_w4_plane_bytes(N, K, group, int(zeros is not None))
     if plane is None:
-        nbytes = lib().pq2_w4_plane_bytes(N, K, group, int(zeros is not None))
         plane = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=codes.device)
+    elif plane.numel() * plane.element_size() < nbytes:
+        raise Pq2Error("pq2_w4_prepare", PQ2_ERR_SHAPE)
     _check("pq2_w4_prepare", lib().pq2_w4_prepare(
         _ptr(codes), codes.stride(0), _ptr(scales), _ptr(zeros), N, K, group, _ptr(plane),
         _stream(stream)))
@@ -525,9 +527,9 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
 _w4_bytes = {}
 
 
-def _check_out(t, shape, *dtypes):
-    if t.shape != shape or not t.is_contiguous() or (dtypes and t.dtype not in dtypes):
-        raise ValueError(f"Expected a contiguous output buffer of shape {shape}")
+def _check_out(t, shape, dtype=None):
+    if t.shape != shape or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"Expected a contiguous output buffer of shape {tuple(shape)}")
 
 
 def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
@@ -545,7 +547,7 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
     key = (N, K, group, zeros)
     if key not in _w4_bytes:
         _w4_bytes[key] = lib().pq2_w4_plane_bytes(N, K, group, int(zeros))
-    if plane.numel() < _w4_bytes[key]:
+    if plane.numel() * plane.element_size() < _w4_bytes[key]:
         raise Pq2Error("pq2_w4_mmv", PQ2_ERR_SHAPE)
     _check("pq2_w4_mmv", lib().pq2_w4_mmv(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, group, int(zeros), _ptr(plane), _ptr(y),
@@ -608,9 +610,11 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
             raise ValueError("gate must have h's type, K columns with unit stride and a row per "
                              "rows_per_gate rows of h")
         ldg = gate.stride(0)
-    for w in (w_pre, w_post):
-        if w is not None and (w.numel() != K or w.dtype != dtype or not w.is_contiguous()):
-            raise ValueError("the norm weights must be contiguous [K] of h's type")
+    if w_pre is not None and (w_pre.numel() != K or w_pre.dtype != dtype
+                              or not w_pre.is_contiguous()) or \
+            w_post is not None and (w_post.numel() != K or w_post.dtype != dtype
+                                    or not w_post.is_contiguous()):
+        raise ValueError("the norm weights must be contiguous [K] of h's type")
     _on_device(z, h, w_pre, w_post, gate, h_out, n_out)
     if h_out is not None:
         _check_out(h_out, shape, dtype)

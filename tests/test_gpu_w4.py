@@ -257,7 +257,9 @@ def test_refusals():
                 lambda: pq2.pq2_w4_mmv(torch.zeros((1, K), device="cuda"), plane, N, 48),
                 lambda: pq2.pq2_w4_mmv(torch.zeros((1, K), device="cuda"), plane, N, G, flags=4),
                 lambda: pq2.pq2_w4_mmv(torch.zeros((1, K), device="cuda"), plane[1:], N, G),
-                lambda: pq2.pq2_w4_mmv(torch.zeros((0, K), device="cuda"), plane, N, G)):
+                lambda: pq2.pq2_w4_mmv(torch.zeros((0, K), device="cuda"), plane, N, G),
+                lambda: pq2.pq2_w4_prepare(codes, scales, z, group=G, plane=plane[16:]),
+                lambda: pq2.pq2_w4_mmv(torch.zeros((1, K), device="cuda"), plane, N + 32, G)):
         with pytest.raises(pq2.Pq2Error):
             bad()
     for bad in (lambda: pq2.pq2_w4_prepare(codes, scales, z, group=128),
