@@ -124,6 +124,7 @@ struct W4Params {
   int M, K, y_dtype;
   int tiles, units;     // of the matrix
   int split;            // CTAs of a cluster, each with a share of the units
+  int warps;            // of the narrow kernel's CTAs
   int block_tiles;      // tiles whose sums the accumulator holds
   int batch_log;        // log2 of the tiles between two joins of the sums
   int vector_x;         // x rows may be read 16 bytes at a time
@@ -392,11 +393,13 @@ __device__ __forceinline__ void store_y(void* y, int dtype, int64_t at, float v)
 
 constexpr int kPitch = 20;  // floats per column of 16 rows: conflict-free
 
-// The narrow kernel's CTA: warps (one pair of units each at a time; a multiple
-// of four, as an SM's four schedulers take warps in turn), CTAs an SM holds
-// (registers and shared memory are bounded for that) and ring stages.
-constexpr int kWarps = 4, kPerSm = 4, kStages = 3;
-constexpr int kSmem = (227 / kPerSm - 1) * 1024;
+// The narrow kernel's CTA: 4, 8, 12 or 16 warps (one pair of units each at a
+// time; multiples of four, as an SM's four schedulers take warps in turn), 16
+// of them an SM (128 registers a thread; shared memory is bounded for that),
+// and ring stages.
+constexpr int kMaxWarps = 16, kStages = 3;
+constexpr int ctas_of(int warps) { return kMaxWarps / warps; }  // an SM
+constexpr int smem_of(int warps) { return (227 / ctas_of(warps) - 1) * 1024; }
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -407,7 +410,7 @@ __device__ __forceinline__ void dependency_wait() {
 }
 
 template <typename XT, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(kWarps * 32, kPerSm) w4_mmv_kernel(const W4Params p) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_mmv_kernel(const W4Params p) {
   constexpr int kParts = parts<XT>();
   constexpr bool kScaled = !std::is_same<XT, __half>::value;
   constexpr int kUnitBytes = unit_bytes(GROUP, ZEROS), kChunks = kUnitBytes / 16;
@@ -835,19 +838,34 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
 }
 
 // The split of K over a cluster orders the additions, so it depends on the
-// matrix and the SM count only.  A CTA's time is its passes times (its tiles +
-// the start of a pass, worth about 6 tiles), and a cluster's join is worth
-// about 4 more; taken where that is least, for a full device.
-int w4_split(int tiles, int units, int sms) {
-  int split = 1;
+// matrix and the SM count only; the warps of the narrow kernel's CTAs come with
+// it.  A CTA's time is its passes times (its tiles + the start of a pass, worth
+// about 6 tiles), and a cluster's join is worth about 4 more; taken where that
+// is least, for a full device.  (Against every other choice, measured: 5120 x
+// 17408 16.3 us, the best 15.1, four warps always 17.4; 1280 x 17408 6.6, 6.5,
+// 8.8; 10240 x 5120 and 4096 x 14336 are the best ones; 131072 x 5120 63.8 and
+// 62.8.)
+struct W4Split {
+  int split, warps;
+};
+W4Split w4_split(int tiles, int units, int sms) {
+  // The last shape's choice: 32 candidates cost as much as the launch's checks.
+  static thread_local struct {
+    int tiles, units, sms;
+    W4Split split;
+  } last{0, 0, 0, {1, 4}};
+  if (last.tiles == tiles && last.units == units && last.sms == sms) return last.split;
+  W4Split best{1, 4};
   int64_t least = INT64_MAX;
-  for (int c = 1; c <= 8 && c <= units; ++c) {
-    const int pairs = ((units + c - 1) / c + 1) / 2, passes = (pairs + kWarps - 1) / kWarps;
-    const int clusters = std::max(1, kPerSm * sms / c);
-    const int64_t cost = (int64_t)passes * ((tiles + clusters - 1) / clusters + 6) + (c > 1 ? 4 : 0);
-    if (cost < least) least = cost, split = c;
-  }
-  return split;
+  for (int w = 4; w <= kMaxWarps; w += 4)
+    for (int c = 1; c <= 8 && c <= units; ++c) {
+      const int pairs = ((units + c - 1) / c + 1) / 2, passes = (pairs + w - 1) / w;
+      const int clusters = std::max(1, ctas_of(w) * sms / c);
+      const int64_t cost = (int64_t)passes * ((tiles + clusters - 1) / clusters + 6) + (c > 1 ? 4 : 0);
+      if (cost < least) least = cost, best = {c, w};
+    }
+  last = {tiles, units, sms, best};
+  return best;
 }
 
 // Clusters of `kern` that fit the device at once, looked up once per device
@@ -869,7 +887,7 @@ int resident_clusters(Kernel kern, std::atomic<int> (&known)[64][9], int split, 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(most, kern, &cfg) != cudaSuccess || *most < 1) {
     cudaGetLastError();
     return PQ2_ERR_CUDA;
@@ -902,12 +920,14 @@ int launch(Kernel kern, const W4Params& p, int clusters, int threads, int smem, 
 
 template <typename XT, int GROUP, bool ZEROS>
 int launch_narrow(W4Params p, cudaStream_t stream) {
-  static std::atomic<int> known[64][9];
+  static std::atomic<int> known[kMaxWarps / 4][64][9];
   auto kern = w4_mmv_kernel<XT, GROUP, ZEROS>;
+  const int room = smem_of(p.warps);
   int most = 0;
-  if (int st = resident_clusters(kern, known, p.split, kWarps * 32, kSmem, &most)) return st;
+  if (int st = resident_clusters(kern, known[p.warps / 4 - 1], p.split, p.warps * 32, room, &most))
+    return st;
   const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
-  const int warps = std::min(kWarps, pairs);
+  const int warps = std::min(p.warps, pairs);
   // Equal shares: the clusters that run at once take as many tiles each.
   const int each = (p.tiles + most - 1) / most;
   const int clusters = (p.tiles + each - 1) / each;
@@ -916,10 +936,10 @@ int launch_narrow(W4Params p, cudaStream_t stream) {
   const int red_tile = warps * cols * kPitch * 4, acc_tile = cols * kTileRows * 4;
   const auto red = [&](int log) { return 2 * (red_tile << log); };
   p.batch_log = 0;
-  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= 8 * 1024 &&
-         ring + red(p.batch_log + 1) + 4 * acc_tile <= kSmem)
+  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= p.warps * 2048 &&
+         ring + red(p.batch_log + 1) + 4 * acc_tile <= room)
     ++p.batch_log;
-  p.block_tiles = std::min(each, (kSmem - ring - red(p.batch_log)) / acc_tile);
+  p.block_tiles = std::min(each, (room - ring - red(p.batch_log)) / acc_tile);
   if (p.block_tiles < 1) return PQ2_ERR_SHAPE;
   return launch(kern, p, clusters, warps * 32,
                 ring + red(p.batch_log) + p.block_tiles * acc_tile, stream);
@@ -1003,7 +1023,8 @@ int launch_w4_mmv(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t N,
   W4Params p{};
   p.x = x, p.plane = plane, p.y = y, p.ldx = ldx, p.N = N, p.K = (int)K, p.y_dtype = y_dtype;
   p.tiles = (int)tiles, p.units = (int)((K + kUnitK - 1) / kUnitK), p.overlap = overlap;
-  p.split = w4_split(p.tiles, p.units, sm_count);
+  const W4Split split = w4_split(p.tiles, p.units, sm_count);
+  p.split = split.split, p.warps = split.warps;
   if (x_dtype == PQ2_BF16) return launch_x<__nv_bfloat16>(p, M, group, zeros, stream);
   if (x_dtype == PQ2_F16) return launch_x<__half>(p, M, group, zeros, stream);
   return launch_x<float>(p, M, group, zeros, stream);
