@@ -936,7 +936,7 @@ int launch_narrow(W4Params p, cudaStream_t stream) {
   const int red_tile = warps * cols * kPitch * 4, acc_tile = cols * kTileRows * 4;
   const auto red = [&](int log) { return 2 * (red_tile << log); };
   p.batch_log = 0;
-  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= p.warps * 2048 &&
+  while (p.batch_log < 3 && 1 << p.batch_log < each && red(p.batch_log + 1) <= p.warps * 4096 &&
          ring + red(p.batch_log + 1) + 4 * acc_tile <= room)
     ++p.batch_log;
   p.block_tiles = std::min(each, (room - ring - red(p.batch_log)) / acc_tile);
