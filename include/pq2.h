@@ -565,7 +565,8 @@ int pq2_w4_prepare(const uint8_t *codes, int64_t ldc, const uint16_t *scales,
  * an fp16 x as it is; a bf16 x scaled by a power of two per 256 columns at
  * most (exact down to 2^-28 of the largest |x| among them, within 2^-39 of it
  * below); a 32-bit x as the sum of two such parts (within 2^-24 of its
- * value).  Products are exact, sums and y fp32.
+ * value).  Products are exact, sums and y fp32.  Infinities and NaN in x come
+ * out as the formula has them.
  *   x        (device, or pinned host memory as for pq2_mmv) x_dtype
  *            [M][ldx], ldx >= K; PQ2_BF16, PQ2_F16 or PQ2_F32.
  *   zeros    non-zero if the plane was prepared with zero points.

@@ -263,7 +263,11 @@ __device__ __forceinline__ float load_b(const XT* x, int64_t k, int64_t K, int p
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
     const int e8 = (int)(__float_as_uint(most) >> 23);
-    const int up = e8 == 255 ? 127 : min(268 - e8, 254);  // 2^(14 - exponent), as a biased exponent
+    // 2^(14 - exponent), as a biased exponent.  Beside an infinity it is the
+    // least of them, so that no finite value becomes another, and a second part
+    // is left out: the first decides the sums.
+    const int up = min(268 - min(e8, 254), 254);
+    const uint32_t kept = part && e8 == 255 ? 0u : 0xFFFFFFFFu;
     const float scale = __uint_as_float((uint32_t)up << 23);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -277,7 +281,7 @@ __device__ __forceinline__ float load_b(const XT* x, int64_t k, int64_t K, int p
           f0 -= __half2float(__float2half_rn(f0));
           f1 -= __half2float(__float2half_rn(f1));
         }
-        r[e] = bits(__floats2half2_rn(f0, f1));
+        r[e] = bits(__floats2half2_rn(f0, f1)) & kept;
       }
       b[j] = make_uint4(r[0], r[1], r[2], r[3]);
     }

@@ -197,6 +197,29 @@ def test_special_values():
     assert bool(y[2].isnan().all()) and not bool(y[3].isfinite().any())
 
 
+@pytest.mark.parametrize("M", [4, 20])
+@pytest.mark.parametrize("dtype,most", [(BF16, 3e38), (F16, 6e4), (F32, 3e38)])
+def test_infinite_x(dtype, most, M):
+    """An infinite x gives the formula's infinities, with their signs, and NaN
+    where the formula does (a weight of zero, infinities of both signs), also
+    next to the largest finite values."""
+    N, K, G = 40, 512, 32
+    codes, scales, z = raw(N, K, G, True, seed=11)
+    scales[3] = 0
+    w = dense(codes, scales, z, G)
+    plane = pq2.pq2_w4_prepare(codes, scales, z, group=G)
+    x = acts(M, K, dtype, seed=12)
+    x[1, 7], x[1, 8], x[1, 9] = float("inf"), -most, most
+    x[2, 300], x[2, 301], x[2, 20] = float("-inf"), -most, 1.0
+    x[3, 7], x[3, 400] = float("inf"), float("-inf")
+    want = (x.double()[1:4, None] * w).sum(2)
+    y = pq2.pq2_w4_mmv(x, plane, N, G, zeros=True, out_dtype=F32)
+    assert not bool(want.isfinite().any()) and bool(want.isinf().any())
+    assert torch.equal(y[1:4].double().nan_to_num(7.0, 1.0, -1.0), want.nan_to_num(7.0, 1.0, -1.0))
+    rest = [0] + list(range(4, M))
+    check(y[rest], x[rest], w)
+
+
 def test_flags_streams_and_capture():
     """Both flags, another stream and a captured graph give the same bits, in
     a chain in which each call reads what the call before it wrote."""
