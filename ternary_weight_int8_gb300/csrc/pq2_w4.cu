@@ -811,10 +811,11 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
       const int rows = min(kRoundTiles, t1 - t0 - n * kRoundTiles) * kTileRows;
       const float* s = sums + (n & 1) * kCols * kRoundPitch;
       // Four rows of a column a thread.
-      for (int e = threadIdx.x - kWideWarps * 32 + rank * kJoinWarps * 32; e < kRoundRows / 4 * p.M;
+      const uint32_t fours = rows / 4;
+      for (uint32_t e = threadIdx.x - kWideWarps * 32 + rank * kJoinWarps * 32; e < fours * p.M;
            e += p.split * kJoinWarps * 32) {
-        const int m = e / (kRoundRows / 4), r = e % (kRoundRows / 4) * 4;
-        if (r >= rows || n0 + r >= p.N) continue;
+        const int m = e / fours, r = e % fours * 4;
+        if (n0 + r >= p.N) continue;
         float4 v[8][kParts];
 #pragma unroll
         for (int z = 0; z < 8; ++z)
