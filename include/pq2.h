@@ -564,8 +564,9 @@ int pq2_w4_prepare(const uint8_t *codes, int64_t ldc, const uint16_t *scales,
 /* pq2_w4_mmv — y = x W^T for M = 1..32.  c - z is exact, x is taken in fp16:
  * an fp16 x as it is; a bf16 x scaled by a power of two per 256 columns at
  * most (exact down to 2^-28 of the largest |x| among them, within 2^-39 of it
- * below); a 32-bit x as the sum of two such parts (within 2^-24 of its
- * value).  Products are exact, sums and y fp32.  Infinities and NaN in x come
+ * below); a 32-bit x as the sum of two such parts (within 2^-23 of its value,
+ * or within 2^-51 of the largest |x| among them where that is more).
+ * Products are exact, sums and y fp32.  Infinities and NaN in x come
  * out as the formula has them.
  *   x        (device, or pinned host memory as for pq2_mmv) x_dtype
  *            [M][ldx], ldx >= K; PQ2_BF16, PQ2_F16 or PQ2_F32.

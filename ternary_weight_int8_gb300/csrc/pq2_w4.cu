@@ -140,8 +140,14 @@ struct W4Params {
 // A bf16 or 32-bit x is scaled by a power of two, one per column and pair of
 // units, so that the pair's largest |x| lies in [2^14, 2^15).  A bf16 value is then
 // exact in fp16 down to 2^-28 of that largest one, and 2^-39 of it is the most
-// that rounding below costs.  A 32-bit x is the sum of two fp16 parts (within
-// 2^-24 of its value), each an MMA column of its own.
+// that rounding below costs.  A 32-bit x is the sum of two fp16 parts, each an
+// MMA column of its own: the first has 11 of its 24 bits, the second at least
+// 11 of the 12 left (2^-23 of the value).  What the first leaves is at most 2^3,
+// so the second has a scale 2^12 times the first's, undone with it after the
+// sums: within 2^-51 of the pair's largest |x| where that is more than 2^-23 of
+// the value.  (Under one scale for both, 2^-39 of the largest; the second scale
+// costs 0.1 us a call.)
+constexpr float kPartScale = 4096.f;
 template <typename XT>
 constexpr int parts() {
   return std::is_same<XT, float>::value ? 2 : 1;
@@ -278,14 +284,16 @@ __device__ __forceinline__ float load_b(const XT* x, int64_t k, int64_t K, int p
       for (int e = 0; e < 4; ++e) {
         float f0 = v[2 * e] * scale, f1 = v[2 * e + 1] * scale;
         if (part) {
-          f0 -= __half2float(__float2half_rn(f0));
-          f1 -= __half2float(__float2half_rn(f1));
+          f0 = (f0 - __half2float(__float2half_rn(f0))) * kPartScale;
+          f1 = (f1 - __half2float(__float2half_rn(f1))) * kPartScale;
         }
         r[e] = bits(__floats2half2_rn(f0, f1)) & kept;
       }
       b[j] = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    return up == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - up) << 23);
+    const float undo =
+        up == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - up) << 23);
+    return part ? undo * (1.f / kPartScale) : undo;
   }
 }
 
