@@ -501,12 +501,20 @@ def _on_device(*tensors):
             raise ValueError("Expected CUDA tensors (or pinned host memory)")
 
 
+def _check_plane(plane):
+    # The kernels take its bytes from the first one on.
+    if plane.dtype != torch.uint8 or not plane.is_contiguous():
+        raise ValueError("plane must be a contiguous uint8 tensor")
+
+
 def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stream=None):
     """4-bit codes u8[N][K/2] (column 2j in the low half of byte j), fp16
     scales [N][K/group] and zero points u8[N][K/group] (None: 8) -> the plane
     u8 that pq2_w4_mmv streams."""
     if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.stride(1) != 1:
         raise ValueError("codes must be a 2-D uint8 tensor with unit column stride")
+    if plane is not None:
+        _check_plane(plane)
     _on_device(codes, scales, zeros, plane)
     N, K = codes.shape[0], 2 * codes.shape[1]
     for t, dt, what in ((scales, torch.float16, "fp16 scales"), (zeros, torch.uint8, "uint8 zeros")):
@@ -516,7 +524,7 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
     nbytes = lib().pq2_w4_plane_bytes(N, K, group, int(zeros is not None))
     if plane is None:
         plane = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=codes.device)
-    elif plane.numel() * plane.element_size() < nbytes:
+    elif plane.numel() < nbytes:
         raise Pq2Error("pq2_w4_prepare", PQ2_ERR_SHAPE)
     _check("pq2_w4_prepare", lib().pq2_w4_prepare(
         _ptr(codes), codes.stride(0), _ptr(scales), _ptr(zeros), N, K, group, _ptr(plane),
@@ -538,6 +546,7 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
     (group and zeros as there)."""
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit column stride")
+    _check_plane(plane)
     M, K = x.shape
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
@@ -547,7 +556,7 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
     key = (N, K, group, zeros)
     if key not in _w4_bytes:
         _w4_bytes[key] = lib().pq2_w4_plane_bytes(N, K, group, int(zeros))
-    if plane.numel() * plane.element_size() < _w4_bytes[key]:
+    if plane.numel() < _w4_bytes[key]:
         raise Pq2Error("pq2_w4_mmv", PQ2_ERR_SHAPE)
     _check("pq2_w4_mmv", lib().pq2_w4_mmv(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, group, int(zeros), _ptr(plane), _ptr(y),
