@@ -515,6 +515,8 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
         raise ValueError("codes must be a 2-D uint8 tensor with unit column stride")
     if plane is not None:
         _check_plane(plane)
+    if group < 1:
+        raise Pq2Error("pq2_w4_prepare", PQ2_ERR_SHAPE)
     _on_device(codes, scales, zeros, plane)
     N, K = codes.shape[0], 2 * codes.shape[1]
     for t, dt, what in ((scales, torch.float16, "fp16 scales"), (zeros, torch.uint8, "uint8 zeros")):
@@ -535,6 +537,13 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
 _w4_bytes = {}
 
 
+def _dtype_of(t):
+    code = _DT.get(t.dtype)
+    if code is None:
+        raise ValueError(f"Expected a bfloat16, float16 or float32 tensor, not {t.dtype}")
+    return code
+
+
 def _check_out(t, shape, dtype=None):
     if t.shape != shape or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"Expected a contiguous output buffer of shape {tuple(shape)}")
@@ -552,6 +561,7 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     else:
         _check_out(y, (M, N))
+    x_dtype, y_dtype = _dtype_of(x), _dtype_of(y)
     _on_device(x, plane, y)
     key = (N, K, group, zeros)
     if key not in _w4_bytes:
@@ -559,8 +569,8 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
     if plane.numel() < _w4_bytes[key]:
         raise Pq2Error("pq2_w4_mmv", PQ2_ERR_SHAPE)
     _check("pq2_w4_mmv", lib().pq2_w4_mmv(
-        _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, group, int(zeros), _ptr(plane), _ptr(y),
-        _DT[y.dtype], flags, _stream(stream)))
+        _ptr(x), x_dtype, x.stride(0), M, N, K, group, int(zeros), _ptr(plane), _ptr(y),
+        y_dtype, flags, _stream(stream)))
     return y
 
 
@@ -571,6 +581,7 @@ def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entr
     top_logprobs [M][k]); `out` is that tuple of buffers."""
     if logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be 2-D with unit column stride")
+    dtype = _dtype_of(logits)
     M, V = logits.shape
     if tokens is not None and (tokens.dtype != torch.int64 or not tokens.is_contiguous()
                                or tokens.shape[0] != M):
@@ -591,7 +602,7 @@ def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entr
         _check_out(out[2], (M, k), torch.int64)
         _check_out(out[3], (M, k), torch.float32)
     _check("pq2_token_logprobs", lib().pq2_token_logprobs(
-        _ptr(logits), _DT[logits.dtype], logits.stride(0), M, V, scale, _ptr(tokens), T,
+        _ptr(logits), dtype, logits.stride(0), M, V, scale, _ptr(tokens), T,
         _ptr(out[0]) if T else None, _ptr(out[1]), k, _ptr(out[2]) if k else None,
         _ptr(out[3]) if k else None, _stream(stream)))
     return out
@@ -607,6 +618,7 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
     dtype = h.dtype
     if h.dim() != 2 or h.stride(1) != 1:
         raise ValueError("h must be 2-D with unit column stride")
+    code = _dtype_of(h)
     M, K = shape = h.shape
     ldz = ldg = 0
     if z is not None:
@@ -634,7 +646,7 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
     elif w_pre is not None:
         n_out = torch.empty((M, K), dtype=dtype, device=h.device)
     _check("pq2_norm_gate_residual", lib().pq2_norm_gate_residual(
-        _ptr(z), ldz, _ptr(h), h.stride(0), _DT[dtype], _ptr(w_post), _ptr(gate), ldg,
+        _ptr(z), ldz, _ptr(h), h.stride(0), code, _ptr(w_post), _ptr(gate), ldg,
         rows_per_gate, alpha, _ptr(w_pre), w_offset, eps, M, K, _ptr(h_out), _ptr(n_out),
         _stream(stream)))
     return h_out, n_out
