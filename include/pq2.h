@@ -577,6 +577,9 @@ int pq2_w4_prepare(const uint8_t *codes, int64_t ldc, const uint16_t *scales,
  *   flags    PQ2_MMV_OVERLAP_WEIGHTS, PQ2_MMV_INDEPENDENT as for pq2_mmv_ex
  *            (plane in the place of codes and scales); the kernel releases
  *            the next one as soon as it starts.
+ * The weights are read once for M <= 8 (4 with a 32-bit x), above that once per
+ * 8 to 32 columns (4 to 16): as many as fit shared memory beside the split of K,
+ * which follows N and K (on 152 SMs 32 for K = 4160 .. 8192, 8 for K = 4096).
  * Column m is bit-identical for every M that contains it: the order of its
  * additions depends on (N, K, group) and the device's SM count only. */
 int pq2_w4_mmv(const void *x, int x_dtype, int64_t ldx, int64_t M, int64_t N,
@@ -605,7 +608,10 @@ int pq2_w4_mmv(const void *x, int x_dtype, int64_t ldx, int64_t M, int64_t N,
  *   k        0 .. min(V, PQ2_MAX_TOP).
  *   top_ids, top_logprobs (device; may be NULL when k = 0) int64 and fp32
  *            [M][k].
- * Sums in fp32 in a fixed order: the same call gives the same bits.  Runs
+ * Sums in fp32 in a fixed order: the same call gives the same bits.  The order
+ * follows M, V and the device's SM count (they decide how many CTAs share a
+ * row), so the log p and entropy of a row may differ in their last bits between
+ * calls with other numbers of rows; the ids do not.  Runs
  * after the kernel before it on the stream and releases the next one as soon
  * as it starts. */
 int pq2_token_logprobs(const void *logits, int dtype, int64_t ldl, int64_t M,

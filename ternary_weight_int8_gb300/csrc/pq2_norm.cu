@@ -11,6 +11,14 @@
 // for their sums.  (4096 rows of 5120 bf16, a gate per token: 36.4 us, 0.85 of
 // the measured copy rate; persistent CTAs with the next two rows' copies in a
 // shared-memory ring took 39.4 us, 160 instead of 320 threads a row 38.3 us.)
+// The choices were made at that width.  Rows of more than 8192 16-bit elements
+// (4096 32-bit ones) load the weights after the first sum, those of more than
+// 16384 (8192) have an SM to themselves, and 64 registers do not hold them
+// whole: 12 to 72 bytes a thread spill with four groups, 204 to 432 with eight
+// (32-bit rows beyond 16384).  Rows, strides or pointers that are not multiples
+// of 16 bytes use narrower accesses.  (500 rows of 20000 bf16 26.7 us, 0.55 of
+// the copy rate; of 20000 fp32 64.4 us, 0.46; of 19999 bf16 70.9 us, 0.21; 4096
+// rows of 5119 bf16 66.6 us, 0.46.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,7 +40,6 @@ struct Pack;
 template <>
 struct Pack<float> {
   static constexpr int E = 4;
-  using Bits = uint32_t;
   static __device__ __forceinline__ void widen(uint4 v, float* f) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
@@ -45,7 +52,6 @@ struct Pack<float> {
 template <>
 struct Pack<__nv_bfloat16> {
   static constexpr int E = 8;
-  using Bits = uint16_t;
   static __device__ __forceinline__ void widen(uint4 v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -67,7 +73,6 @@ struct Pack<__nv_bfloat16> {
 template <>
 struct Pack<__half> {
   static constexpr int E = 8;
-  using Bits = uint16_t;
   static __device__ __forceinline__ void widen(uint4 v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

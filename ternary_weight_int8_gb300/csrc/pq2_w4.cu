@@ -133,7 +133,8 @@ struct W4Params {
 
 // Operands are fp16 whatever x's type: a code OR-ed into the mantissa of 1024
 // is exactly 1024 + c (or 1024 + 16 c, four bits higher), and one fp16
-// operation makes it c - z, exactly.  (bf16 has 7 mantissa bits: the higher
+// operation makes it c - z, exactly (the published way to unpack small whole
+// numbers through a floating-point mantissa).  (bf16 has 7 mantissa bits: the higher
 // field would need a shift of its own, 7 instead of 5 integer operations per
 // 8 weights, and integer operations run at half rate.)
 //
@@ -624,9 +625,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_mmv_kernel(const W4Param
 // The ranges of a cluster are joined round by round by warps of their own,
 // while the others are at the next round: a cluster barrier a round, two sets
 // of sums.  The order of the additions is the narrow kernel's.
-// Bound by mma.sync with fp32 accumulation, about 550 multiply-adds a clock and
-// SM: 131072 x 5120 at M = 32 in 140 us (297 us with 16 columns a launch in the
-// narrow form, 145 us with 8 warps of two tiles).
+// 131072 x 5120 at M = 32 in 140 us (297 us with 16 columns a launch in the
+// narrow form, 145 us with 8 warps of two tiles), 550 multiply-adds a clock and
+// SM: the HMMA pipe at 55 %, shared memory at 70 % (every warp reads all of x's
+// fragments for each unit), and clusters of five leave 12 of 152 SMs without
+// work.  Which of them bounds it was not measured apart.
 constexpr int kWideWarps = 16, kJoinWarps = 4, kWideStages = 4;
 constexpr int kRoundTiles = kWideWarps;
 constexpr int kRoundRows = kRoundTiles * kTileRows;
@@ -854,7 +857,10 @@ __global__ void __launch_bounds__((kWideWarps + kJoinWarps) * 32, 1) w4_wide_ker
 // matrix and the SM count only; the warps of the narrow kernel's CTAs come with
 // it.  A CTA's time is its passes times (its tiles + the start of a pass, worth
 // about 6 tiles), and a cluster's join is worth about 4 more; taken where that
-// is least, for a full device.  (Against every other choice, measured: 5120 x
+// is least, for a full device.  The narrow kernel's passes alone count here:
+// whether the range's fragments fit the wide kernel does not, so for more than
+// 8 columns K = 4096 (16 pairs, split 1) runs 8 at a time and K = 5120 (4 pairs,
+// split 5) 32: 236 against 145 us at M = 32 and 131072 rows.  (Against every other choice, measured: 5120 x
 // 17408 16.3 us, the best 15.1, four warps always 17.4; 1280 x 17408 6.6, 6.5,
 // 8.8; 10240 x 5120 and 4096 x 14336 are the best ones; 131072 x 5120 63.8 and
 // 62.8.)
@@ -965,7 +971,8 @@ int launch_wide(const W4Params& p, cudaStream_t stream) {
   constexpr int kThreads = (kWideWarps + kJoinWarps) * 32;
   int most = 0;
   if (int st = resident_clusters(kern, known, p.split, kThreads, kWideSmem, &most)) return st;
-  // Equal shares, of whole rounds' pairs of tiles.
+  // Equal shares, which need not be whole rounds: a short last round leaves some
+  // warps without a tile.
   const int each = (p.tiles + most - 1) / most;
   const int clusters = (p.tiles + each - 1) / each;
   const int pairs = ((p.units + p.split - 1) / p.split + 1) / 2;
