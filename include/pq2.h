@@ -59,8 +59,9 @@ enum {
   PQ2_ERR_CUDA = 8       /* a CUDA runtime query failed (no device, ...)     */
 };
 
-/* Element types of activations (x) and outputs (y). */
-enum { PQ2_BF16 = 0, PQ2_F16 = 1, PQ2_F32 = 2 };
+/* Element types of activations (x) and outputs (y); PQ2_I8 is the type of an
+ * 8-bit key-value cache (pq2_kv_cache) only. */
+enum { PQ2_BF16 = 0, PQ2_F16 = 1, PQ2_F32 = 2, PQ2_I8 = 3 };
 
 /* Layouts of the quantised activations written by pq2_quantize_act.
  *  PQ2_Q_ROWS   int8 q[M][K], row-major, natural order.
@@ -647,6 +648,144 @@ int pq2_norm_gate_residual(const void *z, int64_t ldz, const void *h,
                            const void *w_pre, float w_offset, float eps,
                            int64_t M, int64_t K, void *h_out, void *n_out,
                            void *stream);
+
+/* A paged key-value cache: the keys and values of `pages` pages of page_size
+ * token slots, for `heads` heads of `dim` elements.
+ *   k, v      (device) dtype; element (page, head, slot, d) lies at
+ *             page * page_stride + head * head_stride + slot * token_stride
+ *             + d, strides in elements and the same for k and v, so that
+ *             [pages][heads][page_size][dim], [pages][page_size][heads][dim]
+ *             and pages that hold k and v in turn are all possible.
+ *   k_scales, v_scales (device, PQ2_I8 only, else NULL) fp32
+ *             [pages][heads][page_size].
+ *   dtype     PQ2_BF16, PQ2_F16 or PQ2_I8: an element of an 8-bit cache
+ *             stands for its integer times the scale of its token and head,
+ *             s = max|x| / 127, q = clamp(round-half-even(x / s), -127, 127)
+ *             (IEEE division; s = 0 divides as 1): pq2_quantize_act's rule
+ *             over the dim elements of a token and head.  An infinity or NaN
+ *             among them reads back as NaN in all of them.
+ *   pages 1 .. 1<<30; heads 1 .. 1<<16; page_size a multiple of 16 up to
+ *   1<<20; dim 64, 128 or 256; k, v and the scales 16-byte aligned, the
+ *   strides multiples of 16 bytes, below 2^40 bytes and not negative; heads,
+ *   slots and pages must not overlap.
+ * A sequence's position p lies in slot p % page_size of page
+ * table[b][p / page_size].  A call that meets an entry that is no page of the
+ * cache, or a position behind the table's width, does not follow it: nothing
+ * is stored there, and it reads as zeros. */
+typedef struct pq2_kv_cache {
+  void *k, *v;
+  float *k_scales, *v_scales;
+  int dtype;
+  int64_t pages, heads, page_size, dim;
+  int64_t page_stride, head_stride, token_stride;
+} pq2_kv_cache;
+
+/* pq2_kv_store — writes the keys and values of the newest tokens of B
+ * sequences into the cache, rounded to nearest even (16 bits) or quantised.
+ * Row i of sequence b, cu[b] <= i < cu[b + 1], is its position
+ *   lens[b] - (cu[b + 1] - cu[b]) + (i - cu[b]):
+ * lens counts the new tokens already.
+ *   k, v     (device) dtype PQ2_BF16, PQ2_F16 or PQ2_F32, element (row, head,
+ *            d) at row * token_stride + head * head_stride + d (strides in
+ *            elements, one pair for each).  Any alignment of whole elements;
+ *            16-byte aligned pointers and strides are faster.
+ *   tokens   rows of k and v, 0 .. 1<<24; rows outside every sequence are
+ *            not read.
+ *   cache    (host) its description; pages, tables and scales are device
+ *            memory.
+ *   table    (device) int32 [B][table_width], rows table_stride apart.
+ *   cu       (device, may be NULL) int32 [B + 1], not decreasing; NULL: the
+ *            rows are split evenly, tokens / B to each (tokens % B = 0).
+ *   lens     (device) int32 [B];  B 1 .. 1<<20.
+ * Two rows for one position are the caller's error: which one stays is not
+ * defined.  Runs after the kernel before it on the stream and releases the
+ * next one as soon as it starts; so does pq2_kv_load. */
+int pq2_kv_store(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                 const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                 int dtype, int64_t tokens, const pq2_kv_cache *cache,
+                 const int32_t *table, int64_t table_stride,
+                 int64_t table_width, const int32_t *cu, const int32_t *lens,
+                 int64_t B, void *stream);
+
+/* pq2_kv_load — the same rows the other way: reads the last
+ * cu[b + 1] - cu[b] positions of each sequence back, packed as
+ * pq2_attn_prefill takes them (with cu the running sums of lens: all of
+ * them).
+ *   k, v     (device) dtype PQ2_BF16, PQ2_F16 or PQ2_F32 [tokens][heads][dim],
+ *            16-byte aligned.  Rows outside every sequence stay as they
+ *            were; a position that is not in the cache gives zeros. */
+int pq2_kv_load(const pq2_kv_cache *cache, const int32_t *table,
+                int64_t table_stride, int64_t table_width, const int32_t *cu,
+                const int32_t *lens, int64_t B, void *k, void *v, int dtype,
+                int64_t tokens, void *stream);
+
+/* pq2_attn_decode — attention of the T newest tokens of each of B sequences
+ * over the cache, which holds their own keys and values already
+ * (pq2_kv_store).  Query head h uses key head h / (q_heads / heads).  With
+ * s_j = scale * q . k_j over the positions j < lens[b] - T + t + 1:
+ *   out[b][t][h] = sum_j exp(s_j) v_j / sum_j exp(s_j)
+ *   lse[b][t][h] = log sum_j exp(s_j)
+ * A row that sees no position (lens[b] = 0, or T > lens[b]) gives 0 and -inf.
+ * Positions that a row does not see take no part, whatever they hold.
+ *   q        (device) dtype PQ2_BF16 or PQ2_F16, element (b, t, h, d) at
+ *            b * batch_stride + t * token_stride + h * head_stride + d
+ *            (elements); 4-byte aligned, even strides.
+ *   cache    of q's dtype, or PQ2_I8.
+ *   q_heads  a multiple of cache->heads, at most 256 times it; T 1 .. 64;
+ *            B 1 .. 1<<16.
+ *   scale    finite.
+ *   out      (device) dtype [B][T][q_heads][dim], 16-byte aligned.
+ *   lse      (device, may be NULL) fp32 [B][T][q_heads].
+ *   workspace (device) pq2_attn_decode_workspace_bytes, 16-byte aligned; its
+ *            contents need not be kept between calls.  Calls that may run at
+ *            the same time need one each.
+ * Scores, the softmax and all sums are fp32.  The weights are rounded to the
+ * type in which the tensor cores take them (a 16-bit cache: q's; an 8-bit one:
+ * fp16), keys and values not at all.  The order of the sums follows B, T,
+ * lens, the heads and the SM count; the same call gives the same bits.
+ * pq2_attn_decode_workspace_bytes returns 0 for invalid arguments. */
+size_t pq2_attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads,
+                                       int64_t heads, int64_t dim);
+int pq2_attn_decode(const void *q, int dtype, int64_t batch_stride,
+                    int64_t token_stride, int64_t head_stride, int64_t B,
+                    int64_t T, int64_t q_heads, const pq2_kv_cache *cache,
+                    const int32_t *table, int64_t table_stride,
+                    int64_t table_width, const int32_t *lens, float scale,
+                    void *out, float *lse, void *workspace,
+                    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* pq2_attn_prefill — attention over packed sequences: rows cu_q[b] ..
+ * cu_q[b + 1] of q attend rows cu_k[b] .. cu_k[b + 1] of k and v.  With
+ * causal, counted from the ends: row t of n_q sees keys j < n_k - n_q + t + 1
+ * (a chunk after what its prompt has so far; n_q = n_k: a whole prompt).
+ * out, lse, scale, heads and the rows that see nothing as in pq2_attn_decode.
+ *   q, k, v  (device) dtype PQ2_BF16 or PQ2_F16, element (row, head, d) at
+ *            row * token_stride + head * head_stride + d; 16-byte aligned,
+ *            strides multiples of 8 elements, below 2^39 and not negative.
+ *   q_heads  a multiple of heads, at most 128 times it; dim 64, 128 or 256.
+ *   q_rows, k_rows  rows of q and of k and v, 1 .. 1<<24 (k_rows may be 0
+ *            when k and v are NULL).
+ *   cu_q, cu_k (device) int32 [B + 1], not decreasing, B 1 .. 1<<16; values
+ *            outside 0 .. rows are taken as the nearest one inside.
+ *   out      (device) dtype [q_rows][q_heads][dim], 16-byte aligned; rows
+ *            outside every sequence stay as they were, in lse as well.
+ *   lse      (device, may be NULL) fp32 [q_rows][q_heads].
+ *   workspace (device) pq2_attn_prefill_workspace_bytes, 16-byte aligned, as
+ *            in pq2_attn_decode; may be NULL where that is 0.
+ * Keys and values that a row does not see take no part, whatever they hold. */
+size_t pq2_attn_prefill_workspace_bytes(int64_t B, int64_t q_rows,
+                                        int64_t k_rows, int64_t q_heads,
+                                        int64_t heads, int64_t dim);
+int pq2_attn_prefill(const void *q, int64_t q_token_stride,
+                     int64_t q_head_stride, const void *k,
+                     int64_t k_token_stride, int64_t k_head_stride,
+                     const void *v, int64_t v_token_stride,
+                     int64_t v_head_stride, int dtype, int64_t q_rows,
+                     int64_t k_rows, int64_t q_heads, int64_t heads,
+                     int64_t dim, const int32_t *cu_q, const int32_t *cu_k,
+                     int64_t B, float scale, int causal, void *out, float *lse,
+                     void *workspace, size_t workspace_bytes,
+                     int32_t *dev_status, void *stream);
 
 /* Paths of pq2_debug_group_dots. */
 enum { PQ2_PATH_MMV_ADDXOR = 0, PQ2_PATH_MM = 1, PQ2_PATH_MMV_PLANES = 2,

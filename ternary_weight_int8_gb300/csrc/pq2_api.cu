@@ -727,4 +727,189 @@ int pq2_norm_gate_residual(const void* z, int64_t ldz, const void* h, int64_t ld
   return pq2::launch_norm(p, dtype, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+bool valid_stride(int64_t s, int bytes) {
+  return s >= 0 && s < ((int64_t)1 << 40) / bytes;
+}
+
+int check_cache(const pq2_kv_cache* c) {
+  if (!c || !c->k || !c->v) return PQ2_ERR_NULL;
+  if (c->dtype != PQ2_BF16 && c->dtype != PQ2_F16 && c->dtype != PQ2_I8) return PQ2_ERR_DTYPE;
+  if (c->dtype == PQ2_I8 && (!c->k_scales || !c->v_scales)) return PQ2_ERR_NULL;
+  if (c->pages < 1 || c->pages > kMaxN || c->heads < 1 || c->heads > 65536 ||
+      c->page_size < 16 || c->page_size % 16 || c->page_size > ((int64_t)1 << 20) ||
+      (c->dim != 64 && c->dim != 128 && c->dim != 256))
+    return PQ2_ERR_SHAPE;
+  const int bytes = c->dtype == PQ2_I8 ? 1 : 2;
+  for (int64_t s : {c->page_stride, c->head_stride, c->token_stride}) {
+    if (!valid_stride(s, bytes)) return PQ2_ERR_SHAPE;
+    if (s * bytes % 16) return PQ2_ERR_ALIGN;
+  }
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return PQ2_ERR_ALIGN;
+  if (c->dtype == PQ2_I8 && (!aligned(c->k_scales, 16) || !aligned(c->v_scales, 16)))
+    return PQ2_ERR_ALIGN;
+  return PQ2_OK;
+}
+
+int check_batch(const int32_t* table, int64_t table_stride, int64_t table_width,
+                const int32_t* cu, const int32_t* lens, int64_t B) {
+  if (!table || !lens) return PQ2_ERR_NULL;
+  if (B < 1 || B > kMaxM || table_width < 1 || table_width > kMaxN ||
+      !valid_ld(table_stride, table_width))
+    return PQ2_ERR_SHAPE;
+  if (!aligned(table, 4) || !aligned(cu, 4) || !aligned(lens, 4)) return PQ2_ERR_ALIGN;
+  return PQ2_OK;
+}
+
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+
+}  // namespace
+
+int pq2_kv_store(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                 int64_t v_token_stride, int64_t v_head_stride, int dtype, int64_t tokens,
+                 const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                 int64_t table_width, const int32_t* cu, const int32_t* lens, int64_t B,
+                 void* stream) {
+  if (!k || !v) return PQ2_ERR_NULL;
+  if (!valid_dtype(dtype)) return PQ2_ERR_DTYPE;
+  if (int st = check_cache(cache)) return st;
+  if (int st = check_batch(table, table_stride, table_width, cu, lens, B)) return st;
+  const int eb = elem_bytes(dtype);
+  if (tokens < 0 || tokens > kMaxRows || (!cu && tokens % B)) return PQ2_ERR_SHAPE;
+  for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+    if (!valid_stride(s, eb)) return PQ2_ERR_SHAPE;
+  if (!aligned(k, eb) || !aligned(v, eb)) return PQ2_ERR_ALIGN;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  if (!tokens) return PQ2_OK;
+  const pq2::KvBatch b{table, cu, lens, table_stride, (int)table_width, (int)B, tokens};
+  return pq2::launch_kv_store({const_cast<void*>(k), k_token_stride, k_head_stride},
+                              {const_cast<void*>(v), v_token_stride, v_head_stride}, dtype,
+                              *cache, b, static_cast<cudaStream_t>(stream));
+}
+
+int pq2_kv_load(const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                int64_t table_width, const int32_t* cu, const int32_t* lens, int64_t B, void* k,
+                void* v, int dtype, int64_t tokens, void* stream) {
+  if (!k || !v) return PQ2_ERR_NULL;
+  if (!valid_dtype(dtype)) return PQ2_ERR_DTYPE;
+  if (int st = check_cache(cache)) return st;
+  if (int st = check_batch(table, table_stride, table_width, cu, lens, B)) return st;
+  if (tokens < 0 || tokens > kMaxRows || (!cu && tokens % B)) return PQ2_ERR_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16)) return PQ2_ERR_ALIGN;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  if (!tokens) return PQ2_OK;
+  const pq2::KvBatch b{table, cu, lens, table_stride, (int)table_width, (int)B, tokens};
+  return pq2::launch_kv_load(*cache, b, k, v, dtype, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+bool valid_decode(int64_t B, int64_t T, int64_t q_heads, int64_t heads, int64_t dim) {
+  return B >= 1 && B <= 65536 && T >= 1 && T <= 64 && heads >= 1 && heads <= 65536 &&
+         q_heads >= heads && q_heads % heads == 0 && q_heads / heads <= 256 &&
+         (dim == 64 || dim == 128 || dim == 256) && B * T * q_heads <= ((int64_t)1 << 31) - 1;
+}
+
+bool is_finite(float x) { return x - x == 0.f; }
+
+}  // namespace
+
+size_t pq2_attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t heads,
+                                       int64_t dim) {
+  if (!valid_decode(B, T, q_heads, heads, dim)) return 0;
+  return pq2::attn_decode_workspace_bytes(B, T, q_heads, heads, dim);
+}
+
+int pq2_attn_decode(const void* q, int dtype, int64_t batch_stride, int64_t token_stride,
+                    int64_t head_stride, int64_t B, int64_t T, int64_t q_heads,
+                    const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                    int64_t table_width, const int32_t* lens, float scale, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (!q || !out || !workspace) return PQ2_ERR_NULL;
+  if (dtype != PQ2_BF16 && dtype != PQ2_F16) return PQ2_ERR_DTYPE;
+  if (int st = check_cache(cache)) return st;
+  if (cache->dtype != dtype && cache->dtype != PQ2_I8) return PQ2_ERR_DTYPE;
+  if (int st = check_batch(table, table_stride, table_width, nullptr, lens, B)) return st;
+  if (!valid_decode(B, T, q_heads, cache->heads, cache->dim) || !is_finite(scale))
+    return PQ2_ERR_SHAPE;
+  for (int64_t s : {batch_stride, token_stride, head_stride}) {
+    if (!valid_stride(s, 2)) return PQ2_ERR_SHAPE;
+    if (s % 2) return PQ2_ERR_ALIGN;
+  }
+  if (!aligned(q, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      !aligned(dev_status, 4))
+    return PQ2_ERR_ALIGN;
+  if (workspace_bytes < pq2::attn_decode_workspace_bytes(B, T, q_heads, cache->heads, cache->dim))
+    return PQ2_ERR_SHAPE;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  pq2::DecodeParams p{};
+  p.q = q, p.dtype = dtype;
+  p.batch_stride = batch_stride, p.token_stride = token_stride, p.head_stride = head_stride;
+  p.T = (int)T, p.q_heads = (int)q_heads;
+  p.batch = {table, nullptr, lens, table_stride, (int)table_width, (int)B, 0};
+  p.scale = scale, p.out = out, p.lse = lse;
+  p.workspace = static_cast<uint8_t*>(workspace), p.status = dev_status;
+  return pq2::launch_attn_decode(p, *cache, sms, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+bool valid_prefill(int64_t B, int64_t q_rows, int64_t k_rows, int64_t q_heads, int64_t heads,
+                   int64_t dim) {
+  return B >= 1 && B <= 65536 && q_rows >= 1 && q_rows <= kMaxRows && k_rows >= 0 &&
+         k_rows <= kMaxRows && heads >= 1 && heads <= 65536 && q_heads >= heads &&
+         q_heads % heads == 0 && q_heads / heads <= 128 &&
+         (dim == 64 || dim == 128 || dim == 256);
+}
+
+}  // namespace
+
+size_t pq2_attn_prefill_workspace_bytes(int64_t B, int64_t q_rows, int64_t k_rows,
+                                        int64_t q_heads, int64_t heads, int64_t dim) {
+  if (!valid_prefill(B, q_rows, k_rows, q_heads, heads, dim)) return 0;
+  return pq2::attn_prefill_workspace_bytes(B, q_rows, k_rows, q_heads, heads, dim);
+}
+
+int pq2_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                     int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                     int64_t v_token_stride, int64_t v_head_stride, int dtype, int64_t q_rows,
+                     int64_t k_rows, int64_t q_heads, int64_t heads, int64_t dim,
+                     const int32_t* cu_q, const int32_t* cu_k, int64_t B, float scale, int causal,
+                     void* out, float* lse, void* workspace, size_t workspace_bytes,
+                     int32_t* dev_status, void* stream) {
+  if (!q || (k_rows && (!k || !v)) || !cu_q || !cu_k || !out) return PQ2_ERR_NULL;
+  if (dtype != PQ2_BF16 && dtype != PQ2_F16) return PQ2_ERR_DTYPE;
+  if (!valid_prefill(B, q_rows, k_rows, q_heads, heads, dim) || !is_finite(scale))
+    return PQ2_ERR_SHAPE;
+  for (int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+                    v_head_stride}) {
+    if (!valid_stride(s, 2)) return PQ2_ERR_SHAPE;
+    if (s % 8) return PQ2_ERR_ALIGN;
+  }
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cu_q, 4) ||
+      !aligned(cu_k, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      !aligned(dev_status, 4))
+    return PQ2_ERR_ALIGN;
+  const size_t need =
+      pq2::attn_prefill_workspace_bytes(B, q_rows, k_rows, q_heads, heads, dim);
+  if (need && !workspace) return PQ2_ERR_NULL;
+  if (workspace_bytes < need) return PQ2_ERR_SHAPE;
+  int sms = 0;
+  if (int st = device_check(&sms)) return st;
+  pq2::PrefillParams p{};
+  p.q = {const_cast<void*>(q), q_token_stride, q_head_stride};
+  p.k = {const_cast<void*>(k), k_token_stride, k_head_stride};
+  p.v = {const_cast<void*>(v), v_token_stride, v_head_stride};
+  p.dtype = dtype, p.q_rows = q_rows, p.k_rows = k_rows;
+  p.q_heads = (int)q_heads, p.heads = (int)heads, p.dim = (int)dim;
+  p.cu_q = cu_q, p.cu_k = cu_k, p.B = (int)B;
+  p.scale = scale, p.causal = causal != 0, p.out = out, p.lse = lse;
+  p.workspace = static_cast<uint8_t*>(workspace), p.status = dev_status;
+  return pq2::launch_attn_prefill(p, sms, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

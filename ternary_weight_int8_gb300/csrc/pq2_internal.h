@@ -119,4 +119,57 @@ struct NormParams {
 };
 int launch_norm(const NormParams& p, int dtype, cudaStream_t stream);
 
+// The key-value cache and its attention.  A batch of sequences: the page
+// table and the lengths, and for packed rows the running sums cu (NULL: the
+// same number of rows for each).
+struct KvBatch {
+  const int32_t *table, *cu, *lens;
+  int64_t table_stride;
+  int table_width, B;
+  int64_t rows;
+};
+struct KvRows {
+  void* p;
+  int64_t token_stride, head_stride;
+};
+int launch_kv_store(KvRows k, KvRows v, int dtype, const pq2_kv_cache& c, const KvBatch& b,
+                    cudaStream_t stream);
+int launch_kv_load(const pq2_kv_cache& c, const KvBatch& b, void* k, void* v, int dtype,
+                   cudaStream_t stream);
+
+struct DecodeParams {
+  const void* q;
+  int dtype;
+  int64_t batch_stride, token_stride, head_stride;
+  int T, q_heads;
+  KvBatch batch;  // rows unused
+  float scale;
+  void* out;
+  float* lse;
+  uint8_t* workspace;
+  int32_t* status;
+};
+size_t attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t heads,
+                                   int64_t dim);
+int launch_attn_decode(const DecodeParams& p, const pq2_kv_cache& c, int sm_count,
+                       cudaStream_t stream);
+
+struct PrefillParams {
+  KvRows q, k, v;
+  int dtype;
+  int64_t q_rows, k_rows;
+  int q_heads, heads, dim;
+  const int32_t *cu_q, *cu_k;
+  int B;
+  float scale;
+  int causal;
+  void* out;
+  float* lse;
+  uint8_t* workspace;
+  int32_t* status;
+};
+size_t attn_prefill_workspace_bytes(int64_t B, int64_t q_rows, int64_t k_rows, int64_t q_heads,
+                                    int64_t heads, int64_t dim);
+int launch_attn_prefill(const PrefillParams& p, int sm_count, cudaStream_t stream);
+
 }  // namespace pq2

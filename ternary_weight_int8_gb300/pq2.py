@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -23,7 +24,7 @@ LIB_PATH = os.path.join(_PKG, "libpq2.so")
 
 PQ2_OK, PQ2_ERR_NULL, PQ2_ERR_SHAPE, PQ2_ERR_ALIGN, PQ2_ERR_DTYPE = 0, 1, 2, 3, 4
 PQ2_ERR_ARCH, PQ2_ERR_LAUNCH, PQ2_ERR_TIMEOUT, PQ2_ERR_CUDA = 5, 6, 7, 8
-PQ2_BF16, PQ2_F16, PQ2_F32 = 0, 1, 2
+PQ2_BF16, PQ2_F16, PQ2_F32, PQ2_I8 = 0, 1, 2, 3
 PQ2_Q_ROWS, PQ2_Q_PLANES, PQ2_Q_F16, PQ2_Q_F8, PQ2_Q_MMV16 = 0, 1, 2, 3, 4
 PQ2_DECODE_ADDXOR, PQ2_DECODE_PLANES = 0, 1
 PQ2_PATH_MMV_ADDXOR, PQ2_PATH_MM, PQ2_PATH_MMV_PLANES, PQ2_PATH_MM_F8, PQ2_PATH_MMV_TC = \
@@ -33,6 +34,17 @@ PQ2_STATIC_SCRATCH_BYTES = 1 << 20
 PQ2_MAX_TOP = 32
 PQ2_PREP_MAX_K = 32768
 GROUP = 128
+
+
+
+class CKvCache(ctypes.Structure):
+    """pq2_kv_cache of include/pq2.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
 
 # C signatures, mirroring include/pq2.h.
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -78,6 +90,16 @@ SIGNATURES = {
                                 _P, _P, _P]),
     "pq2_norm_gate_residual": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _I64, _I64, ctypes.c_float,
                                     _P, ctypes.c_float, ctypes.c_float, _I64, _I64, _P, _P, _P]),
+    "pq2_kv_store": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _P, _P,
+                          _I64, _P]),
+    "pq2_kv_load": (_I, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _I, _I64, _P]),
+    "pq2_attn_decode_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "pq2_attn_decode": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P,
+                             ctypes.c_float, _P, _P, _P, _SZ, _P, _P]),
+    "pq2_attn_prefill_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "pq2_attn_prefill": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I64,
+                              _I64, _I64, _I64, _P, _P, _I64, ctypes.c_float, _I, _P, _P, _P,
+                              _SZ, _P, _P]),
     "pq2_mmv_geometry": (_I, [_I64, _I64, _I, _P, _P, _P, _P]),
     "pq2_debug_mmv_drop_arrival": (_I, [_P, _P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I64, _P,
                                         _P]),
@@ -650,6 +672,221 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
         rows_per_gate, alpha, _ptr(w_pre), w_offset, eps, M, K, _ptr(h_out), _ptr(n_out),
         _stream(stream)))
     return h_out, n_out
+
+
+class KVCache(NamedTuple):
+    """The pages of a key-value cache: k and v [pages][heads][page_size][dim]
+    (bfloat16, float16 or int8; any equal strides, unit for dim), and for int8
+    their scales fp32 [pages][heads][page_size]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
+
+
+def kv_cache(pages: int, heads: int, page_size: int, dim: int, dtype=torch.int8, device="cuda"):
+    """A new, empty KVCache."""
+    shape = (pages, heads, page_size, dim)
+    if dtype not in _CACHE_DT:
+        raise ValueError("Expected an int8, float16 or bfloat16 cache")
+    scales = [torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)] \
+        if dtype == torch.int8 else (None, None)
+    return KVCache(torch.zeros(shape, dtype=dtype, device=device),
+                   torch.zeros(shape, dtype=dtype, device=device), *scales)
+
+
+_CACHE_DT = {torch.bfloat16: PQ2_BF16, torch.float16: PQ2_F16, torch.int8: PQ2_I8}
+
+
+def _strides(t):
+    """Strides for the C ABI: those of dimensions with one element are never
+    walked, and torch leaves anything in them."""
+    return [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]
+
+
+def _c_cache(cache):
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _CACHE_DT or \
+            k.stride(3) != 1 or v.stride(3) != 1 or _strides(k) != _strides(v):
+        raise ValueError("a cache's k and v must be 4-D int8, float16 or bfloat16 tensors of one "
+                         "shape and strides, with unit stride in dim")
+    if (k.dtype == torch.int8) != (ks is not None) or (ks is None) != (vs is None):
+        raise ValueError("an int8 cache has scales, others have none")
+    for t in (ks, vs):
+        if t is not None and (t.dtype != torch.float32 or t.shape != k.shape[:3]
+                              or not t.is_contiguous()):
+            raise ValueError("the scales must be contiguous float32 [pages][heads][page_size]")
+    st = _strides(k)
+    return CKvCache(_ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _CACHE_DT[k.dtype], k.shape[0],
+                    k.shape[1], k.shape[2], k.shape[3], st[0], st[1], st[2])
+
+
+def _check_ints(t, what, n=None):
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+            n is not None and t.shape[0] != n:
+        raise ValueError(f"{what} must be contiguous int32" + (f" [{n}]" if n is not None else ""))
+
+
+def _check_table(table, lens, cu=None):
+    """The batch's size, after the checks of its page table and lengths."""
+    if table.dim() != 2 or table.dtype != torch.int32 or \
+            (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError("table must be 2-D int32 with unit column stride")
+    B = table.shape[0]
+    _check_ints(lens, "lens", B)
+    if cu is not None:
+        _check_ints(cu, "cu", B + 1)
+    return B
+
+
+def _table_stride(table):
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def _on_one_device(*tensors):
+    """CUDA tensors of one device, the current one (whose stream is used)."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("Expected CUDA tensors")
+        if device is None:
+            device = t.device
+            if device.index != (_device() if _device else torch.cuda.current_device()):
+                raise ValueError("the tensors' device must be the current device")
+        elif t.device != device:
+            raise ValueError("Expected tensors of one device")
+
+
+def _rows_of_heads(t, what, heads=None, dim=None):
+    if t.dim() != 3 or t.stride(2) != 1 or heads is not None and t.shape[1] != heads or \
+            dim is not None and t.shape[2] != dim:
+        raise ValueError(f"{what} must be [rows][heads][dim] with unit stride in dim")
+
+
+def pq2_kv_store(k, v, cache: KVCache, table, lens, cu=None, stream=None):
+    """Writes the newest tokens' keys and values k, v [tokens][heads][dim] into
+    the cache: sequence b's rows cu[b]..cu[b+1] (cu None: the rows split evenly)
+    are its last positions before lens[b]; page table[b][p // page_size] holds
+    position p."""
+    c = _c_cache(cache)
+    _rows_of_heads(k, "k", c.heads, c.dim)
+    _rows_of_heads(v, "v", c.heads, c.dim)
+    dtype = _dtype_of(k)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must have one shape and type")
+    B = _check_table(table, lens, cu)
+    _on_one_device(k, v, *cache, table, lens, cu)
+    ks, vs = _strides(k), _strides(v)
+    _check("pq2_kv_store", lib().pq2_kv_store(
+        _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], dtype, k.shape[0], ctypes.addressof(c),
+        _ptr(table), _table_stride(table), table.shape[1], _ptr(cu), _ptr(lens), B,
+        _stream(stream)))
+
+
+def pq2_kv_load(cache: KVCache, table, lens, cu=None, tokens=None, out=None,
+                out_dtype=torch.bfloat16, stream=None):
+    """The last cu[b+1] - cu[b] positions of each sequence, read back and packed
+    -> (k, v) [tokens][heads][dim]; `out` is that pair of buffers, else `tokens`
+    gives their rows."""
+    c = _c_cache(cache)
+    B = _check_table(table, lens, cu)
+    if out is None:
+        if tokens is None:
+            raise ValueError("either out or tokens must be given")
+        out = [torch.empty((tokens, c.heads, c.dim), dtype=out_dtype, device=cache.k.device)
+               for _ in range(2)]
+    k, v = out
+    shape = (k.shape[0] if tokens is None else tokens, c.heads, c.dim)
+    dtype = _dtype_of(k)
+    _check_out(k, shape)
+    _check_out(v, shape, k.dtype)
+    _on_one_device(k, v, *cache, table, lens, cu)
+    _check("pq2_kv_load", lib().pq2_kv_load(
+        ctypes.addressof(c), _ptr(table), _table_stride(table), table.shape[1], _ptr(cu),
+        _ptr(lens), B, _ptr(k), _ptr(v), dtype, shape[0], _stream(stream)))
+    return k, v
+
+
+def _attn_outputs(q, out, lse):
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"Expected a bfloat16 or float16 tensor, not {q.dtype}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _check_out(out, q.shape, q.dtype)
+    if lse is not None:
+        _check_out(lse, q.shape[:-1], torch.float32)
+    return out
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=None,
+                    workspace=None, status=None, stream=None):
+    """Attention of the newest token(s) of each sequence over its cache, which
+    holds their keys and values already: q [B][heads][dim] or [B][T][heads][dim]
+    -> out of q's shape.  Token t of T sees the positions before
+    lens[b] - T + t + 1.  scale: 1 / sqrt(dim) if None; lse: a float32 buffer of
+    q.shape[:-1] for the rows' log-sum-exp."""
+    c = _c_cache(cache)
+    if q.dim() not in (3, 4) or q.stride(-1) != 1 or q.shape[-1] != c.dim:
+        raise ValueError("q must be [B][heads][dim] or [B][T][heads][dim] with unit stride in dim")
+    B = _check_table(table, lens)
+    if q.shape[0] != B:
+        raise ValueError("q must have a row per row of the table")
+    out = _attn_outputs(q, out, lse)
+    T, heads = (1, q.shape[1]) if q.dim() == 3 else (q.shape[1], q.shape[2])
+    if cache.k.dtype not in (q.dtype, torch.int8):
+        raise ValueError("the cache must have q's type, or int8")
+    nbytes = lib().pq2_attn_decode_workspace_bytes(B, T, heads, c.heads, c.dim)
+    workspace = _workspace(workspace, nbytes, q.device)
+    _on_one_device(q, *cache, table, lens, out, lse, workspace, status)
+    st = _strides(q)
+    _check("pq2_attn_decode", lib().pq2_attn_decode(
+        _ptr(q), _DT[q.dtype], st[0], st[1] if q.dim() == 4 else 0, st[-2], B, T, heads,
+        ctypes.addressof(c), _ptr(table), _table_stride(table), table.shape[1], _ptr(lens),
+        c.dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
+    return out
+
+
+def pq2_attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal: bool = True, out=None,
+                     lse=None, workspace=None, status=None, stream=None):
+    """Attention over packed sequences: rows cu_q[b]..cu_q[b+1] of q
+    [rows][heads][dim] attend rows cu_k[b]..cu_k[b+1] (None: the same) of k and
+    v [rows][key heads][dim]; causal counts both from their ends.  scale and lse
+    as in pq2_attn_decode."""
+    _rows_of_heads(q, "q")
+    _rows_of_heads(k, "k", None, q.shape[2])
+    _rows_of_heads(v, "v", k.shape[1], q.shape[2])
+    if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v must have one shape, and q's type")
+    cu_k = cu_q if cu_k is None else cu_k
+    _check_ints(cu_q, "cu_q")
+    _check_ints(cu_k, "cu_k", cu_q.shape[0])
+    out = _attn_outputs(q, out, lse)
+    rows, heads, dim = q.shape
+    keys, kv_heads, B = k.shape[0], k.shape[1], cu_q.shape[0] - 1
+    nbytes = lib().pq2_attn_prefill_workspace_bytes(B, rows, keys, heads, kv_heads, dim)
+    if workspace is not None or nbytes:
+        workspace = _workspace(workspace, nbytes, q.device)
+    _on_one_device(q, k, v, cu_q, cu_k, out, lse, workspace, status)
+    qs, ks, vs = _strides(q), _strides(k), _strides(v)
+    _check("pq2_attn_prefill", lib().pq2_attn_prefill(
+        _ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _DT[q.dtype], rows,
+        keys, heads, kv_heads, dim, _ptr(cu_q), _ptr(cu_k), B,
+        dim ** -0.5 if scale is None else scale, int(causal), _ptr(out), _ptr(lse),
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _ptr(status), _stream(stream)))
+    return out
 
 
 def mmv_geometry(N: int, K: int, sm_count: int):
