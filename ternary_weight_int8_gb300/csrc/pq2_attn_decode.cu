@@ -1,5 +1,4 @@
-// pq2_attn.cu — attention of new tokens over a paged cache and of packed
-// prompts over their keys.
+// pq2_attn_decode.cu — attention of new tokens over a paged cache.
 //
 // A warp takes one query row and walks its keys with the running maximum m
 // and sum l of a softmax: for a score s (in units of ln 2) the new maximum is
@@ -92,37 +91,6 @@ __global__ void __launch_bounds__(128) decode_kernel(const DecodeParams p, const
                  p.lse ? p.lse + item : nullptr);
 }
 
-template <typename QT, int D>
-__global__ void __launch_bounds__(128) prefill_kernel(const PrefillParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= p.q_rows * p.q_heads) return;
-  const int h = (int)(item % p.q_heads);
-  const int64_t i = item / p.q_heads;
-  int lo = 0, hi = p.B + 1;  // how many sums are <= i
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(p.cu_q + mid) <= i) lo = mid + 1; else hi = mid;
-  }
-  const int b = lo - 1;
-  if (b < 0 || b >= p.B) return;
-  const auto clamped = [](int64_t x, int64_t n) { return x < 0 ? 0 : x > n ? n : x; };
-  const int64_t q0 = clamped(__ldg(p.cu_q + b), p.q_rows), nq = clamped(__ldg(p.cu_q + b + 1), p.q_rows) - q0;
-  const int64_t k0 = clamped(__ldg(p.cu_k + b), p.k_rows), nk = clamped(__ldg(p.cu_k + b + 1), p.k_rows) - k0;
-  const int64_t kh = h / (p.q_heads / p.heads);
-  const int64_t most = p.causal ? nk - nq + (i - q0) + 1 : nk;
-  const auto key = [&](int64_t j, const QT** k, const QT** v, float* ks, float* vs) {
-    *k = static_cast<const QT*>(p.k.p) + (k0 + j) * p.k.token_stride + kh * p.k.head_stride;
-    *v = static_cast<const QT*>(p.v.p) + (k0 + j) * p.v.token_stride + kh * p.v.head_stride;
-    *ks = *vs = 1.f;
-    return true;
-  };
-  row<QT, QT, D>(static_cast<const QT*>(p.q.p) + i * p.q.token_stride + h * p.q.head_stride,
-                 p.scale, most, key, static_cast<QT*>(p.out) + item * D,
-                 p.lse ? p.lse + item : nullptr);
-}
-
 template <typename K, typename... A>
 int launch(K kernel, int64_t rows, cudaStream_t stream, const A&... args) {
   if ((rows + 3) / 4 > 0x7fffffff) return PQ2_ERR_SHAPE;
@@ -150,20 +118,9 @@ int launch_decode(const DecodeParams& p, const pq2_kv_cache& c, cudaStream_t str
   return launch(decode_kernel<QT, CT, 256>, rows, stream, p, c);
 }
 
-template <typename QT>
-int launch_prefill(const PrefillParams& p, cudaStream_t stream) {
-  const int64_t rows = p.q_rows * p.q_heads;
-  if (p.dim == 64) return launch(prefill_kernel<QT, 64>, rows, stream, p);
-  if (p.dim == 128) return launch(prefill_kernel<QT, 128>, rows, stream, p);
-  return launch(prefill_kernel<QT, 256>, rows, stream, p);
-}
-
 }  // namespace
 
 size_t attn_decode_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 16; }
-size_t attn_prefill_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
-  return 0;
-}
 
 int launch_attn_decode(const DecodeParams& p, const pq2_kv_cache& c, int sm_count,
                        cudaStream_t stream) {
@@ -173,12 +130,6 @@ int launch_attn_decode(const DecodeParams& p, const pq2_kv_cache& c, int sm_coun
                              : launch_decode<__nv_bfloat16, __nv_bfloat16>(p, c, stream);
   return c.dtype == PQ2_I8 ? launch_decode<__half, int8_t>(p, c, stream)
                            : launch_decode<__half, __half>(p, c, stream);
-}
-
-int launch_attn_prefill(const PrefillParams& p, int sm_count, cudaStream_t stream) {
-  (void)sm_count;
-  return p.dtype == PQ2_BF16 ? launch_prefill<__nv_bfloat16>(p, stream)
-                             : launch_prefill<__half>(p, stream);
 }
 
 }  // namespace pq2

@@ -1,0 +1,646 @@
+// pq2_attn_prefill.cu — attention over packed sequences on the tcgen05 tensor
+// cores (sm_103a).
+//
+// Per query row, with scores s_j = c q . k_j (c = scale / ln 2) over the keys
+// that it sees, out = sum 2^(s_j - m) v_j / sum 2^(s_j - m): the keys pass by
+// once in tiles of 128, m is a running maximum.  m may stay up to 8 below the
+// true one (weights up to 256): only a rise beyond that scales the sums that
+// are already there, which happens in the first tiles and hardly after them.
+//
+// A CTA takes kTiles = 2 query tiles of 128 rows (1 for dim 256) of one key
+// head.  A tile's rows are tokens x the G query heads of that key head, row =
+// token * G + head, so grouped heads share every key tile that is loaded and a
+// short chunk still fills the tile.
+//   warps 0-3 (0-7)  softmax, one row a thread and four warps a tile: scores
+//            from tensor memory, maximum, weights rounded to 16 bits and stored
+//            over the scores, sums in fp32; at the end the output
+//   next     copies: Q once, then K and V pieces (128 keys x 128 columns at
+//            most) through a ring in shared memory
+//   last     allocates tensor memory and issues the MMAs: scores = Q K^T (both
+//            from shared memory, K-major), out += P V (P from tensor memory, V
+//            as it lies, its keys along K: MN-major)
+// While the softmax works on one tile's scores the tensor cores have the other
+// tile's two products (dim 256: the next key tile's scores, in a second
+// buffer, and the last one's P V), so neither waits for the other for long.
+//
+// Bound: the MMAs, 4 * 128 * 128 * dim operations a tile pair of 128 x 128.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "pq2_internal.h"
+#include "pq2_tensor.cuh"
+
+namespace pq2 {
+namespace {
+
+constexpr int BM = 128, BN = 128;  // rows of a query tile, keys of a key tile
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;  // how far m may stay behind, in powers of two
+
+template <int D>
+struct Geo {
+  static constexpr int tiles = D <= 128 ? 2 : 1;    // query tiles of a CTA
+  static constexpr int slots = 2;                   // score buffers
+  static constexpr int cols = D < 128 ? D : 128;    // columns of a ring piece
+  static constexpr int pieces = D / cols;           // pieces of a key tile
+  static constexpr int piece = BN * cols * 2;       // bytes
+  static constexpr int stages = D < 128 ? 8 : 5;
+  static constexpr int qBytes = BM * D * 2;         // of one tile
+  static constexpr int offRing = tiles * qBytes;
+  static constexpr int offBar = offRing + stages * piece;
+  static constexpr int smem = offBar + 512 + 1024;  // + barriers, alignment
+  static constexpr int threads = tiles * 128 + 64;
+  static constexpr int copyWarp = tiles * 4, mmaWarp = copyWarp + 1;
+  static constexpr int oCol = slots * BN;           // tensor memory columns
+  static_assert(oCol + tiles * D <= 512, "tensor memory");
+  static_assert(smem <= 227 * 1024, "shared memory");
+};
+
+struct Params {
+  const int32_t *cu_q, *cu_k;
+  const void *q, *k, *v;  // for single rows, where the copies do not serve
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  void* out;
+  float* lse;
+  int32_t* status;
+  int B, q_rows, k_rows, q_heads, heads, group, tokens;  // tokens of a query tile
+  float c;        // |scale| / ln 2
+  int negative;   // scale < 0
+  int causal;
+};
+
+// Shared-memory matrix descriptor of a 128-byte swizzled operand whose M or N
+// dimension is the contiguous one: 64 elements x 8 rows of K a core block,
+// blocks of K 1024 bytes apart, the next 64 elements `next` bytes on.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t next) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(next >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// As mma_f16_ta, A from shared memory.
+__device__ __forceinline__ void mma_f16_ss(uint32_t on, uint32_t d_tmem, uint64_t adesc,
+                                           uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+        "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+        "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// (a0, a1) * b + c in both halves.
+__device__ __forceinline__ void fma2(float& r0, float& r1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+      "mov.b64 c, {%5, %5};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& r0, float& r1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\t"
+      "add.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(r0), "+f"(r1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+constexpr uint32_t kFormat = std::is_same<T, __half>::value ? 0u : 1u;
+template <typename T>
+__device__ constexpr uint32_t instr_desc(int n, bool b_mn_major, bool negate_a) {
+  return (1u << 4) | kFormat<T> << 7 | kFormat<T> << 10 | (negate_a ? 1u << 13 : 0u) |
+         (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+}
+
+// 32 columns of one row by the formula itself, for rows whose sums met an
+// infinity or NaN: the MMA multiplies every value of a key tile by its weight,
+// and 0 * NaN of a key that the row does not see would stay in the row.
+template <typename T, int D>
+__device__ __noinline__ void plain_columns(const T* q, const T* k, int64_t k_token, const T* v,
+                                           int64_t v_token, int most, float c, float mc,
+                                           float factor, T* out) {
+#pragma unroll 1
+  for (int d0 = 0; d0 < 32; d0 += 8) {
+    float o[8] = {};
+#pragma unroll 1
+    for (int j = 0; j < most; ++j) {
+      float s = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; ++d) s = fmaf(widen(q[d]), widen(k[(int64_t)j * k_token + d]), s);
+      const float p = ex2(fmaf(s, c, -mc));
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[d] = fmaf(p, widen(v[(int64_t)j * v_token + d0 + d]), o[d]);
+    }
+    uint4 w;
+    w.x = pack<T>(o[0] * factor, o[1] * factor), w.y = pack<T>(o[2] * factor, o[3] * factor);
+    w.z = pack<T>(o[4] * factor, o[5] * factor), w.w = pack<T>(o[6] * factor, o[7] * factor);
+    *reinterpret_cast<uint4*>(out + d0) = w;
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Geo<D>::threads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const Params p) {
+  using G = Geo<D>;
+  constexpr int kTiles = G::tiles, kStages = G::stages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_s = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::offBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;   // per query tile
+  uint64_t* s_full = q_full + kTiles;   // per score buffer
+  uint64_t* p_full = s_full + G::slots;
+  uint64_t* o_full = p_full + G::slots; // per query tile
+  uint32_t* tmem_addr_s = reinterpret_cast<uint32_t*>(o_full + kTiles);
+  int* sums = reinterpret_cast<int*>(tmem_addr_s + 1);  // per warp, then the CTA's place
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kWarps = G::threads / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // Which sequence and which of its query tiles: the CTAs count them from the
+  // last one back, so that of one long prompt the tiles with the most keys come
+  // first.  A sequence of n rows has ceil(n / (kTiles * tokens)).
+  const int per = kTiles * p.tokens;
+  const int head = blockIdx.x % p.heads, nth = blockIdx.x / p.heads;
+  const auto row_of = [&](const int32_t* cu, int i, int rows) {
+    return min(max(__ldg(cu + i), 0), rows);
+  };
+  int seq = -1, tile = 0;
+  {
+    int* place = sums + kWarps;
+    if (tid == 0) place[0] = -1;
+    int behind = 0;  // tiles of the sequences behind those looked at
+    for (int last = p.B; last > 0 && behind <= nth; last -= G::threads) {
+      const int b = last - 1 - tid;
+      int n = 0;
+      if (b >= 0) n = max(row_of(p.cu_q, b + 1, p.q_rows) - row_of(p.cu_q, b, p.q_rows), 0);
+      n = (n + per - 1) / per;
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      int before = behind;
+      for (int w = 0; w < warp; ++w) before += sums[w];
+      upto += before;
+      if (nth < upto && nth >= upto - n) place[0] = b, place[1] = upto - 1 - nth;
+      behind = upto;
+      if (tid == G::threads - 1) place[2] = behind;
+      __syncthreads();
+      behind = place[2];
+      __syncthreads();
+    }
+    __syncthreads();
+    seq = place[0], tile = place[1];
+    __syncthreads();
+  }
+  if (seq < 0) return;
+
+  const int q0 = row_of(p.cu_q, seq, p.q_rows);
+  const int nq = row_of(p.cu_q, seq + 1, p.q_rows) - q0;
+  const int k0 = row_of(p.cu_k, seq, p.k_rows);
+  const int nk = max(row_of(p.cu_k, seq + 1, p.k_rows) - k0, 0);
+  // The keys that token t sees.
+  const auto sees = [&](int t) { return p.causal ? min(max(nk - nq + t + 1, 0), nk) : nk; };
+  int first[kTiles], count[kTiles], most_tiles = 0;  // first token, key tiles
+#pragma unroll
+  for (int s = 0; s < kTiles; ++s) {
+    first[s] = (tile * kTiles + s) * p.tokens;
+    count[s] = first[s] < nq ? (sees(min(first[s] + p.tokens, nq) - 1) + BN - 1) / BN : 0;
+    most_tiles = max(most_tiles, count[s]);
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < kTiles; ++i) mbar_init(&q_full[i], 1), mbar_init(&o_full[i], 1);
+    for (int i = 0; i < G::slots; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+    fence_barrier_init();
+  }
+  if (warp == G::mmaWarp) {
+    tmem_alloc(tmem_addr_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_addr_s;
+  bool ok = true;
+
+  // The ring holds the pieces in the order in which the MMAs use them: a key
+  // tile's K, then the V of the tile before (dim 256: one further behind).
+  if (warp == G::copyWarp) {
+    if (lane == 0 && most_tiles > 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+      int use = 0;
+      const auto pieces = [&](const CUtensorMap* map, int j) {
+        for (int i = 0; i < G::pieces; ++i, ++use) {
+          const int st = use % kStages;
+          if (use >= kStages) ok = ok && mbar_wait(&empty[st], (use / kStages - 1) & 1);
+          mbar_arrive_expect_tx(&full[st], G::piece);
+          uint8_t* to = smem + G::offRing + st * G::piece;
+          for (int x = 0; x < G::cols / 64; ++x)
+            tma_3d(to + x * (BN * 128), map, i * G::cols + x * 64, head, k0 + j * BN, &full[st]);
+        }
+      };
+#pragma unroll
+      for (int s = 0; s < kTiles; ++s) {
+        if (!count[s]) continue;
+        mbar_arrive_expect_tx(&q_full[s], p.tokens * p.group * D * 2);
+        for (int x = 0; x < D / 64; ++x)
+          tma_3d(smem + s * G::qBytes + x * (BM * 128), &map_q, x * 64, head * p.group,
+                 q0 + first[s], &q_full[s]);
+        if (s == 0) pieces(&map_k, 0);
+      }
+      if (!count[0]) pieces(&map_k, 0);
+      for (int j = 0; j < most_tiles; ++j) {
+        if (kTiles == 2) {
+          pieces(&map_v, j);
+          if (j + 1 < most_tiles) pieces(&map_k, j + 1);
+        } else {
+          if (j + 1 < most_tiles) pieces(&map_k, j + 1);
+          pieces(&map_v, j);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == G::mmaWarp) {
+    const uint32_t on = elect_one();
+    constexpr uint32_t idesc_pv = instr_desc<T>(G::cols, true, false);
+    const uint32_t idesc_qk = instr_desc<T>(BN, false, p.negative);
+    const uint32_t ring = smem_u32(smem + G::offRing);
+    int k_use = 0, v_use = 0;  // ring positions of the K and V in use
+    // Scores of tile s against the K pieces at ring position `use`.
+    const auto scores = [&](int s, int slot, int use, bool release) {
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem + s * G::qBytes));
+#pragma unroll
+      for (int i = 0; i < G::pieces; ++i) {
+        const int st = (use + i) % kStages;
+        ok = ok && mbar_wait(&full[st], ((use + i) / kStages) & 1);
+        tc_fence_after();
+        const uint64_t kd = smem_desc_sw128(ring + st * G::piece);
+#pragma unroll
+        for (int x = 0; x < G::cols / 16; ++x) {
+          const int d = i * G::cols + x * 16;
+          const uint64_t qo = ((d / 64) * (BM * 128) + (d % 64) * 2) >> 4;
+          const uint64_t ko = ((x / 4) * (BN * 128) + (x % 4) * 32) >> 4;
+          mma_f16_ss(on, tmem + slot * BN, qd + qo, kd + ko, idesc_qk, i > 0 || x > 0);
+        }
+        if (release) mma_commit(on, &empty[st]);
+      }
+      mma_commit(on, &s_full[slot]);
+    };
+    // out += P V of tile s, V's pieces at ring position `use`.
+    const auto product = [&](int s, int slot, int use, int j, bool release, bool clean) {
+      ok = ok && mbar_wait(&p_full[slot], (kTiles == 2 ? j : j / 2) & 1);
+#pragma unroll
+      for (int i = 0; i < G::pieces; ++i) {
+        const int st = (use + i) % kStages;
+        ok = ok && mbar_wait(&full[st], ((use + i) / kStages) & 1);
+        if (clean) {
+          // The keys behind the sequence's last one are another sequence's, or
+          // nothing: their values may be infinite or NaN, and the MMA would
+          // multiply those by a weight of zero.
+          for (int x = 0; x < G::cols / 64; ++x)
+            for (int r = nk - j * BN + lane / 8; r < BN; r += 4)
+              *reinterpret_cast<uint4*>(smem + G::offRing + st * G::piece + x * (BN * 128) +
+                                        r * 128 + (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        tc_fence_after();
+        const uint64_t vd = smem_desc_mn(ring + st * G::piece, BN * 128);
+#pragma unroll
+        for (int x = 0; x < BN / 16; ++x)
+          mma_f16_ta(on, tmem + G::oCol + s * D + i * G::cols, tmem + slot * BN + x * 8,
+                     vd + ((x * 2048) >> 4), idesc_pv, j > 0 || x > 0);
+        if (release) mma_commit(on, &empty[st]);
+      }
+      mma_commit(on, &o_full[s]);
+    };
+    const auto ragged = [&](int j) { return (j + 1) * BN > nk; };
+    if (most_tiles > 0) {
+      if constexpr (kTiles == 2) {
+        // positions: K0 V0 K1 V1 ...; the last tile that uses a piece frees it
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!count[s]) continue;
+          ok = ok && mbar_wait(&q_full[s], 0);
+          scores(s, s, 0, s == 1 || count[1] == 0);
+        }
+        for (int j = 0; j < most_tiles; ++j) {
+          k_use = (2 * j + 2) * G::pieces, v_use = (2 * j + 1) * G::pieces;
+          bool cleaned = false;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (j >= count[s]) continue;
+            product(s, s, v_use, j, s == 1 || j >= count[1], ragged(j) && !cleaned);
+            cleaned = true;
+            if (j + 1 < count[s]) scores(s, s, k_use, s == 1 || j + 1 >= count[1]);
+          }
+        }
+      } else {
+        // positions: K0 K1 V0 K2 V1 ...
+        ok = ok && mbar_wait(&q_full[0], 0);
+        scores(0, 0, 0, true);
+        int use = G::pieces;
+        for (int j = 0; j < most_tiles; ++j) {
+          if (j + 1 < most_tiles) {
+            scores(0, (j + 1) & 1, use, true);
+            use += G::pieces;
+          }
+          product(0, j & 1, use, j, true, ragged(j));
+          use += G::pieces;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int s = warp / 4, r = tid % 128, tiles = s ? count[kTiles - 1] : count[0];
+    const int t0 = s ? first[kTiles - 1] : first[0], t = t0 + r / p.group;
+    const bool live = r < p.tokens * p.group && t < nq;
+    const int most = live ? sees(t) : 0;  // keys of this row
+    // All rows of the tile see the keys before this.
+    const int common = sees(t0);
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t o_tmem = tmem + lanes + G::oCol + s * D;
+    float m = -INFINITY, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+    for (int j = 0; j < tiles; ++j) {
+      const int slot = kTiles == 2 ? s : j & 1;
+      const uint32_t s_tmem = tmem + lanes + slot * BN;
+      ok = ok && mbar_wait(&s_full[slot], (kTiles == 2 ? j : j / 2) & 1);
+      tc_fence_after();
+      float v[BN];
+#pragma unroll
+      for (int i = 0; i < BN / 32; ++i) tmem_ld32(s_tmem + 32 * i, v + 32 * i);
+      tmem_ld_wait();
+      if ((j + 1) * BN > common) {
+        const int end = most - j * BN;
+#pragma unroll
+        for (int i = 0; i < BN; ++i) v[i] = i < end ? v[i] : -INFINITY;
+      }
+      float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int i = 4; i < BN - 4; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], v[i + e], v[i + 4 + e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[BN - 4 + e]);
+      const float high = max3(top[0], top[1], fmaxf(top[2], top[3]));
+      if (j == 0) {
+        m = high;
+      } else {
+        const bool rise = (high - m) * p.c > kSlack;
+        if (__any_sync(~0u, rise)) {
+          const float f = rise ? ex2((m - high) * p.c) : 1.f;
+          if (rise) m = high;
+          l0 *= f, l1 *= f, l2 *= f, l3 *= f;
+          ok = ok && mbar_wait(&o_full[s], (j - 1) & 1);
+          tc_fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_tmem + d, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(o_tmem + d, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float mc = m == -INFINITY ? 0.f : m * p.c;
+#pragma unroll
+      for (int i = 0; i < BN; i += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          float a, b, c, d;
+          fma2(a, b, v[i + e], v[i + e + 1], p.c, -mc);
+          fma2(c, d, v[i + e + 2], v[i + e + 3], p.c, -mc);
+          a = ex2(a), b = ex2(b), c = ex2(c), d = ex2(d);
+          add2(l0, l1, a, b);
+          add2(l2, l3, c, d);
+          w[e / 2] = pack<T>(a, b), w[e / 2 + 1] = pack<T>(c, d);
+        }
+        tmem_st16(s_tmem + i / 2, w);
+      }
+      tmem_st_wait();
+      // With one tile the last product but one may still be running here; a
+      // phase further and the wait for the last one could not tell them apart.
+      if (kTiles == 1 && j > 0 && j + 1 == tiles) ok = ok && mbar_wait(&o_full[0], (j - 1) & 1);
+      tc_fence_before();
+      __syncwarp();
+      warp_arrive(&p_full[slot]);
+    }
+    const float l = (l0 + l1) + (l2 + l3);
+    if (tiles) {
+      ok = ok && mbar_wait(&o_full[s], (tiles - 1) & 1);
+      tc_fence_after();
+    }
+    const int h = head * p.group + r % p.group;
+    const int64_t row = ((int64_t)q0 + t) * p.q_heads + h;
+    T* out = static_cast<T*>(p.out) + row * D;
+    const float factor = most > 0 ? 1.f / l : 0.f;
+    const float mc = m == -INFINITY ? 0.f : m * p.c;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 32) {
+      float o[32];
+      __syncwarp();
+      if (tiles) {
+        tmem_ld32(o_tmem + d, o);
+        tmem_ld_wait();
+      }
+      float zero = 0.f;  // NaN if an element is not finite
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (most <= 0) o[i] = 0.f;
+        zero = fmaf(o[i], 0.f, zero);
+      }
+      if (!live) continue;
+      if (zero != 0.f && factor - factor == 0.f) {
+        const T* q = static_cast<const T*>(p.q) + ((int64_t)q0 + t) * p.q_token + h * p.q_head;
+        const T* k = static_cast<const T*>(p.k) + (int64_t)k0 * p.k_token + head * p.k_head;
+        const T* v = static_cast<const T*>(p.v) + (int64_t)k0 * p.v_token + head * p.v_head + d;
+        plain_columns<T, D>(q, k, p.k_token, v, p.v_token, most, p.negative ? -p.c : p.c, mc,
+                            factor, out + d);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        uint4 w;
+        w.x = pack<T>(o[i] * factor, o[i + 1] * factor);
+        w.y = pack<T>(o[i + 2] * factor, o[i + 3] * factor);
+        w.z = pack<T>(o[i + 4] * factor, o[i + 5] * factor);
+        w.w = pack<T>(o[i + 6] * factor, o[i + 7] * factor);
+        *reinterpret_cast<uint4*>(out + d + i) = w;
+      }
+    }
+    if (live && p.lse)
+      p.lse[row] = most > 0 ? mc * kLn2 + logf(l) : -INFINITY;
+  }
+  if (!ok) report(p.status, PQ2_ERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == G::mmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- host
+// Rows of `heads` heads of D 16-bit elements, boxes of 64 elements x box_heads
+// x box_rows.
+bool row_map(CUtensorMap* map, const KvRows& r, int64_t rows, int heads, int dim, int dtype,
+             int box_heads, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  // Strides of dimensions with one element are never walked, but must be valid.
+  const cuuint64_t head = (cuuint64_t)(heads > 1 ? r.head_stride : dim) * 2;
+  const cuuint64_t token = (cuuint64_t)(rows > 1 ? r.token_stride : (int64_t)heads * dim) * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {head, token};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(map,
+             dtype == PQ2_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             3, r.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+int launch(const PrefillParams& a, cudaStream_t stream) {
+  using G = Geo<D>;
+  auto kern = prefill_kernel<T, D>;
+  static bool configured = false;
+  if (!configured) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return PQ2_ERR_LAUNCH;
+    }
+    configured = true;
+  }
+  Params p{};
+  p.cu_q = a.cu_q, p.cu_k = a.cu_k;
+  p.q = a.q.p, p.k = a.k.p, p.v = a.v.p;
+  p.q_token = a.q.token_stride, p.q_head = a.q.head_stride;
+  p.k_token = a.k.token_stride, p.k_head = a.k.head_stride;
+  p.v_token = a.v.token_stride, p.v_head = a.v.head_stride;
+  p.out = a.out, p.lse = a.lse, p.status = a.status;
+  p.B = a.B, p.q_rows = (int)a.q_rows, p.k_rows = (int)a.k_rows;
+  p.q_heads = a.q_heads, p.heads = a.heads, p.group = a.q_heads / a.heads;
+  p.tokens = BM / p.group;
+  // A scale of zero as one that is too small to matter: a key that is not seen
+  // has the score -infinity, and 0 times that is NaN.
+  p.c = std::max(std::fabs(a.scale) * kLog2e, 1e-38f);
+  p.negative = a.scale < 0.f;
+  p.causal = a.causal;
+  CUtensorMap mq, mk, mv;
+  // Without keys no copy is made; the maps then describe q.
+  const KvRows& k = a.k_rows ? a.k : a.q;
+  const KvRows& v = a.k_rows ? a.v : a.q;
+  const int64_t rows = a.k_rows ? a.k_rows : a.q_rows;
+  const int heads = a.k_rows ? a.heads : a.q_heads;
+  if (!row_map(&mq, a.q, a.q_rows, a.q_heads, D, a.dtype, p.group, p.tokens) ||
+      !row_map(&mk, k, rows, heads, D, a.dtype, 1, BN) ||
+      !row_map(&mv, v, rows, heads, D, a.dtype, 1, BN))
+    return PQ2_ERR_LAUNCH;
+  // As many tiles as the sequences can have at most.
+  const int per = G::tiles * p.tokens;
+  const int64_t tiles = std::min<int64_t>(a.q_rows, (a.q_rows + per - 1) / per + a.B - 1);
+  if (tiles * a.heads > 0x7fffffff) return PQ2_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * a.heads));
+  cfg.blockDim = dim3(G::threads);
+  cfg.dynamicSmemBytes = G::smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PQ2_ERR_LAUNCH;
+  }
+  return PQ2_OK;
+}
+
+template <typename T>
+int launch_dim(const PrefillParams& p, cudaStream_t stream) {
+  if (p.dim == 64) return launch<T, 64>(p, stream);
+  if (p.dim == 128) return launch<T, 128>(p, stream);
+  return launch<T, 256>(p, stream);
+}
+
+}  // namespace
+
+size_t attn_prefill_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
+  return 0;
+}
+
+int launch_attn_prefill(const PrefillParams& p, int sm_count, cudaStream_t stream) {
+  (void)sm_count;
+  return p.dtype == PQ2_BF16 ? launch_dim<__nv_bfloat16>(p, stream)
+                             : launch_dim<__half>(p, stream);
+}
+
+}  // namespace pq2
