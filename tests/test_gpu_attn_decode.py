@@ -180,6 +180,29 @@ def test_infinity_and_nan_where_they_are_seen(cache_dtype):
     assert not bool(out[0, 0].isnan().any() or out[0, 1, :2].isnan().any() or out[1].isnan().any())
 
 
+@pytest.mark.parametrize("dtype,cache_dtype", KINDS)
+@pytest.mark.parametrize("n", [40, 3000])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_of_positions_that_only_later_tokens_see(dtype, cache_dtype, n, bad):
+    """The newest position's value is not finite: the tokens before it do not see
+    it, whatever slice, part or join it passes through."""
+    lens = [n, 29]
+    cache, table, dense = A.make_cache(2, lens, 2, 16, 64, cache_dtype, seed=3)
+    page, slot = int(table[0, (n - 1) // 16]), (n - 1) % 16
+    if cache_dtype == I8:
+        cache.v_scales[page, 1, slot] = bad
+    else:
+        cache.v[page, 1, slot, 5:9] = bad
+    q = queries(2, 3, 8, 64, dtype, seed=1)
+    out = pq2.pq2_attn_decode(q, cache, table, ints(lens))
+    assert not bool(out[0, 2, 4:, 5:9].isfinite().any())
+    clean = [[x.clone() for x in d] for d in dense]
+    for b, rows in ((0, slice(0, 2)), (1, slice(0, 3))):
+        T = rows.stop
+        verify(out[b:b + 1, rows].contiguous(), None, q[b:b + 1, rows], cache,
+               [lens[b] - 3 + T], [[x[:, :lens[b] - 3 + T] for x in clean[b]]])
+
+
 def test_pages_outside_the_cache_read_as_zeros():
     lens = [64, 50]
     cache, table, dense = A.make_cache(2, lens, 2, 16, 64, BF16, seed=3)
