@@ -736,16 +736,19 @@ int pq2_kv_load(const pq2_kv_cache *cache, const int32_t *table,
  *   scale    finite.
  *   out      (device) dtype [B][T][q_heads][dim], 16-byte aligned.
  *   lse      (device, may be NULL) fp32 [B][T][q_heads].
- *   workspace (device) pq2_attn_decode_workspace_bytes, 16-byte aligned; its
- *            contents need not be kept between calls.  Calls that may run at
- *            the same time need one each.
+ *   workspace (device) pq2_attn_decode_workspace_bytes (positions =
+ *            table_width * page_size), 16-byte aligned; NULL where that is 0.
+ *            Its contents need not be kept between calls.  Calls that may run
+ *            at the same time need one each.
  * Scores, the softmax and all sums are fp32.  The weights are rounded to the
  * type in which the tensor cores take them (a 16-bit cache: q's; an 8-bit one:
  * fp16), keys and values not at all.  The order of the sums follows B, T,
  * lens, the heads and the SM count; the same call gives the same bits.
- * pq2_attn_decode_workspace_bytes returns 0 for invalid arguments. */
+ * pq2_attn_decode_workspace_bytes returns 0 for few heads and short tables,
+ * which need none, and for invalid arguments. */
 size_t pq2_attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads,
-                                       int64_t heads, int64_t dim);
+                                       int64_t heads, int64_t dim,
+                                       int64_t positions);
 int pq2_attn_decode(const void *q, int dtype, int64_t batch_stride,
                     int64_t token_stride, int64_t head_stride, int64_t B,
                     int64_t T, int64_t q_heads, const pq2_kv_cache *cache,

@@ -818,9 +818,9 @@ bool is_finite(float x) { return x - x == 0.f; }
 }  // namespace
 
 size_t pq2_attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t heads,
-                                       int64_t dim) {
-  if (!valid_decode(B, T, q_heads, heads, dim)) return 0;
-  return pq2::attn_decode_workspace_bytes(B, T, q_heads, heads, dim);
+                                       int64_t dim, int64_t positions) {
+  if (!valid_decode(B, T, q_heads, heads, dim) || positions < 0) return 0;
+  return pq2::attn_decode_workspace_bytes(B, T, q_heads, heads, dim, positions);
 }
 
 int pq2_attn_decode(const void* q, int dtype, int64_t batch_stride, int64_t token_stride,
@@ -828,7 +828,7 @@ int pq2_attn_decode(const void* q, int dtype, int64_t batch_stride, int64_t toke
                     const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
                     int64_t table_width, const int32_t* lens, float scale, void* out, float* lse,
                     void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
-  if (!q || !out || !workspace) return PQ2_ERR_NULL;
+  if (!q || !out) return PQ2_ERR_NULL;
   if (dtype != PQ2_BF16 && dtype != PQ2_F16) return PQ2_ERR_DTYPE;
   if (int st = check_cache(cache)) return st;
   if (cache->dtype != dtype && cache->dtype != PQ2_I8) return PQ2_ERR_DTYPE;
@@ -842,8 +842,10 @@ int pq2_attn_decode(const void* q, int dtype, int64_t batch_stride, int64_t toke
   if (!aligned(q, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(dev_status, 4))
     return PQ2_ERR_ALIGN;
-  if (workspace_bytes < pq2::attn_decode_workspace_bytes(B, T, q_heads, cache->heads, cache->dim))
-    return PQ2_ERR_SHAPE;
+  const size_t need = pq2::attn_decode_workspace_bytes(B, T, q_heads, cache->heads, cache->dim,
+                                                       table_width * cache->page_size);
+  if (need && !workspace) return PQ2_ERR_NULL;
+  if (workspace_bytes < need) return PQ2_ERR_SHAPE;
   int sms = 0;
   if (int st = device_check(&sms)) return st;
   pq2::DecodeParams p{};

@@ -150,7 +150,7 @@ struct DecodeParams {
   int32_t* status;
 };
 size_t attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_t heads,
-                                   int64_t dim);
+                                   int64_t dim, int64_t positions);
 int launch_attn_decode(const DecodeParams& p, const pq2_kv_cache& c, int sm_count,
                        cudaStream_t stream);
 

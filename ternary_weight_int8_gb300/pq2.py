@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -93,7 +94,7 @@ SIGNATURES = {
     "pq2_kv_store": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _P, _P,
                           _I64, _P]),
     "pq2_kv_load": (_I, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _I, _I64, _P]),
-    "pq2_attn_decode_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "pq2_attn_decode_workspace_bytes": (_SZ, [_I64] * 6),
     "pq2_attn_decode": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P,
                              ctypes.c_float, _P, _P, _P, _SZ, _P, _P]),
     "pq2_attn_prefill_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
@@ -704,21 +705,33 @@ def _strides(t):
     return [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]
 
 
+# pq2_kv_cache as bytes: cheaper to make than a ctypes structure.
+_KV_CACHE = struct.Struct("@PPPPiqqqqqqq")
+
+
 def _c_cache(cache):
+    """(pq2_kv_cache, heads, dim) of a KVCache, after the checks."""
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _CACHE_DT or \
-            k.stride(3) != 1 or v.stride(3) != 1 or _strides(k) != _strides(v):
+    shape, st, code = k.shape, k.stride(), _CACHE_DT.get(k.dtype)
+    if code is None or len(shape) != 4 or v.shape != shape or v.dtype != k.dtype or \
+            st[3] != 1 or (v.stride() != st and (v.stride(3) != 1 or _strides(k) != _strides(v))):
         raise ValueError("a cache's k and v must be 4-D int8, float16 or bfloat16 tensors of one "
                          "shape and strides, with unit stride in dim")
-    if (k.dtype == torch.int8) != (ks is not None) or (ks is None) != (vs is None):
-        raise ValueError("an int8 cache has scales, others have none")
-    for t in (ks, vs):
-        if t is not None and (t.dtype != torch.float32 or t.shape != k.shape[:3]
-                              or not t.is_contiguous()):
-            raise ValueError("the scales must be contiguous float32 [pages][heads][page_size]")
-    st = _strides(k)
-    return CKvCache(_ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _CACHE_DT[k.dtype], k.shape[0],
-                    k.shape[1], k.shape[2], k.shape[3], st[0], st[1], st[2])
+    if code != PQ2_I8:
+        if ks is not None or vs is not None:
+            raise ValueError("an int8 cache has scales, others have none")
+        sides = 0, 0
+    else:
+        if ks is None or vs is None:
+            raise ValueError("an int8 cache has scales, others have none")
+        for t in (ks, vs):
+            if t.dtype != torch.float32 or t.shape != shape[:3] or not t.is_contiguous():
+                raise ValueError("the scales must be contiguous float32 [pages][heads][page_size]")
+        sides = ks.data_ptr(), vs.data_ptr()
+    if 1 in shape:
+        st = _strides(k)
+    return _KV_CACHE.pack(k.data_ptr(), v.data_ptr(), *sides, code, *shape, *st[:3]), shape[1], \
+        shape[3]
 
 
 def _check_ints(t, what, n=None):
@@ -728,40 +741,33 @@ def _check_ints(t, what, n=None):
 
 
 def _check_table(table, lens, cu=None):
-    """The batch's size, after the checks of its page table and lengths."""
-    if table.dim() != 2 or table.dtype != torch.int32 or \
-            (table.stride(1) != 1 and table.shape[1] > 1):
+    """(B, row stride, width) of a page table, after the checks of a batch."""
+    shape = table.shape
+    if len(shape) != 2 or table.dtype != torch.int32 or (table.stride(1) != 1 and shape[1] > 1):
         raise ValueError("table must be 2-D int32 with unit column stride")
-    B = table.shape[0]
+    B, width = shape
     _check_ints(lens, "lens", B)
     if cu is not None:
         _check_ints(cu, "cu", B + 1)
-    return B
+    return B, table.stride(0) if B > 1 else width, width
 
 
-def _table_stride(table):
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
-
-
-def _on_one_device(*tensors):
+def _on_one_device(first, *others):
     """CUDA tensors of one device, the current one (whose stream is used)."""
-    device = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("Expected CUDA tensors")
-        if device is None:
-            device = t.device
-            if device.index != (_device() if _device else torch.cuda.current_device()):
-                raise ValueError("the tensors' device must be the current device")
-        elif t.device != device:
-            raise ValueError("Expected tensors of one device")
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            device = -1
+    if device < 0:
+        raise ValueError("Expected CUDA tensors of one device")
+    if device != (torch.cuda.current_device() if _device is None else _device()):
+        raise ValueError("the tensors' device must be the current device")
 
 
 def _rows_of_heads(t, what, heads=None, dim=None):
-    if t.dim() != 3 or t.stride(2) != 1 or heads is not None and t.shape[1] != heads or \
-            dim is not None and t.shape[2] != dim:
+    shape = t.shape
+    if len(shape) != 3 or t.stride(2) != 1 or heads is not None and shape[1] != heads or \
+            dim is not None and shape[2] != dim:
         raise ValueError(f"{what} must be [rows][heads][dim] with unit stride in dim")
 
 
@@ -770,19 +776,18 @@ def pq2_kv_store(k, v, cache: KVCache, table, lens, cu=None, stream=None):
     the cache: sequence b's rows cu[b]..cu[b+1] (cu None: the rows split evenly)
     are its last positions before lens[b]; page table[b][p // page_size] holds
     position p."""
-    c = _c_cache(cache)
-    _rows_of_heads(k, "k", c.heads, c.dim)
-    _rows_of_heads(v, "v", c.heads, c.dim)
+    c, heads, dim = _c_cache(cache)
+    _rows_of_heads(k, "k", heads, dim)
+    _rows_of_heads(v, "v", heads, dim)
     dtype = _dtype_of(k)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must have one shape and type")
-    B = _check_table(table, lens, cu)
+    B, stride, width = _check_table(table, lens, cu)
     _on_one_device(k, v, *cache, table, lens, cu)
     ks, vs = _strides(k), _strides(v)
     _check("pq2_kv_store", lib().pq2_kv_store(
-        _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], dtype, k.shape[0], ctypes.addressof(c),
-        _ptr(table), _table_stride(table), table.shape[1], _ptr(cu), _ptr(lens), B,
-        _stream(stream)))
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dtype, k.shape[0], c,
+        table.data_ptr(), stride, width, _ptr(cu), lens.data_ptr(), B, _stream(stream)))
 
 
 def pq2_kv_load(cache: KVCache, table, lens, cu=None, tokens=None, out=None,
@@ -790,22 +795,22 @@ def pq2_kv_load(cache: KVCache, table, lens, cu=None, tokens=None, out=None,
     """The last cu[b+1] - cu[b] positions of each sequence, read back and packed
     -> (k, v) [tokens][heads][dim]; `out` is that pair of buffers, else `tokens`
     gives their rows."""
-    c = _c_cache(cache)
-    B = _check_table(table, lens, cu)
+    c, heads, dim = _c_cache(cache)
+    B, stride, width = _check_table(table, lens, cu)
     if out is None:
         if tokens is None:
             raise ValueError("either out or tokens must be given")
-        out = [torch.empty((tokens, c.heads, c.dim), dtype=out_dtype, device=cache.k.device)
+        out = [torch.empty((tokens, heads, dim), dtype=out_dtype, device=cache.k.device)
                for _ in range(2)]
     k, v = out
-    shape = (k.shape[0] if tokens is None else tokens, c.heads, c.dim)
+    shape = (k.shape[0] if tokens is None else tokens, heads, dim)
     dtype = _dtype_of(k)
     _check_out(k, shape)
     _check_out(v, shape, k.dtype)
     _on_one_device(k, v, *cache, table, lens, cu)
     _check("pq2_kv_load", lib().pq2_kv_load(
-        ctypes.addressof(c), _ptr(table), _table_stride(table), table.shape[1], _ptr(cu),
-        _ptr(lens), B, _ptr(k), _ptr(v), dtype, shape[0], _stream(stream)))
+        c, table.data_ptr(), stride, width, _ptr(cu), lens.data_ptr(), B, k.data_ptr(),
+        v.data_ptr(), dtype, shape[0], _stream(stream)))
     return k, v
 
 
@@ -821,14 +826,6 @@ def _attn_outputs(q, out, lse):
     return out
 
 
-def _workspace(workspace, nbytes, device):
-    if workspace is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace
-
-
 def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=None,
                     workspace=None, status=None, stream=None):
     """Attention of the newest token(s) of each sequence over its cache, which
@@ -836,25 +833,32 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
     -> out of q's shape.  Token t of T sees the positions before
     lens[b] - T + t + 1.  scale: 1 / sqrt(dim) if None; lse: a float32 buffer of
     q.shape[:-1] for the rows' log-sum-exp."""
-    c = _c_cache(cache)
-    if q.dim() not in (3, 4) or q.stride(-1) != 1 or q.shape[-1] != c.dim:
+    L = lib()
+    c, kv_heads, dim = _c_cache(cache)
+    shape, st = q.shape, _strides(q)
+    if len(shape) not in (3, 4) or q.stride(-1) != 1 or shape[-1] != dim:
         raise ValueError("q must be [B][heads][dim] or [B][T][heads][dim] with unit stride in dim")
-    B = _check_table(table, lens)
-    if q.shape[0] != B:
+    B, stride, width = _check_table(table, lens)
+    if shape[0] != B:
         raise ValueError("q must have a row per row of the table")
     out = _attn_outputs(q, out, lse)
-    T, heads = (1, q.shape[1]) if q.dim() == 3 else (q.shape[1], q.shape[2])
+    T, T_stride = (1, 0) if len(shape) == 3 else (shape[1], st[1])
     if cache.k.dtype not in (q.dtype, torch.int8):
         raise ValueError("the cache must have q's type, or int8")
-    nbytes = lib().pq2_attn_decode_workspace_bytes(B, T, heads, c.heads, c.dim)
-    workspace = _workspace(workspace, nbytes, q.device)
+    if workspace is None:
+        nbytes = L.pq2_attn_decode_workspace_bytes(B, T, shape[-2], kv_heads, dim,
+                                                   width * cache.k.shape[2])
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _on_one_device(q, *cache, table, lens, out, lse, workspace, status)
-    st = _strides(q)
-    _check("pq2_attn_decode", lib().pq2_attn_decode(
-        _ptr(q), _DT[q.dtype], st[0], st[1] if q.dim() == 4 else 0, st[-2], B, T, heads,
-        ctypes.addressof(c), _ptr(table), _table_stride(table), table.shape[1], _ptr(lens),
-        c.dim ** -0.5 if scale is None else scale, _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
+    _check("pq2_attn_decode", L.pq2_attn_decode(
+        q.data_ptr(), _DT[q.dtype], st[0], T_stride, st[-2], B, T, shape[-2], c,
+        table.data_ptr(), stride, width, lens.data_ptr(), dim ** -0.5 if scale is None else scale,
+        out.data_ptr(), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream)))
     return out
 
 
@@ -876,8 +880,10 @@ def pq2_attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal: bool = True, 
     rows, heads, dim = q.shape
     keys, kv_heads, B = k.shape[0], k.shape[1], cu_q.shape[0] - 1
     nbytes = lib().pq2_attn_prefill_workspace_bytes(B, rows, keys, heads, kv_heads, dim)
-    if workspace is not None or nbytes:
-        workspace = _workspace(workspace, nbytes, q.device)
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _on_one_device(q, k, v, cu_q, cu_k, out, lse, workspace, status)
     qs, ks, vs = _strides(q), _strides(k), _strides(v)
     _check("pq2_attn_prefill", lib().pq2_attn_prefill(

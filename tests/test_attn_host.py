@@ -45,6 +45,16 @@ CACHES = [(dict(k=None), NULL), (dict(v=None), NULL), (dict(k_scales=None), NULL
           (dict(dtype=pq2.PQ2_F16, k_scales=None, v_scales=None, token_stride=132), ALIGN)]
 
 
+def test_the_cache_s_layout():
+    cache = pq2.kv_cache(7, 3, 16, 64, device="cpu")
+    packed, heads, dim = pq2._c_cache(cache)
+    c = pq2.CKvCache.from_buffer_copy(packed)
+    assert len(packed) == ctypes.sizeof(pq2.CKvCache) and (heads, dim) == (3, 64)
+    assert (c.k, c.v, c.k_scales, c.v_scales) == tuple(t.data_ptr() for t in cache)
+    assert (c.dtype, c.pages, c.heads, c.page_size, c.dim) == (pq2.PQ2_I8, 7, 3, 16, 64)
+    assert (c.page_stride, c.head_stride, c.token_stride) == cache.k.stride()[:3]
+
+
 def test_caches(L):
     decode = lambda c: L.pq2_attn_decode(  # noqa: E731
         A, pq2.PQ2_BF16, 512, 512, 128, 1, 1, 4, c, A, 4, 4, A, 1.0, A, None, A, 1 << 40, None, None)
@@ -81,7 +91,7 @@ def test_store_and_load_refusals(L):
 
 def test_decode_refusals(L):
     c = c_cache()
-    ok = [A, pq2.PQ2_BF16, 512, 512, 128, 1, 1, 4, ctypes.addressof(c), A, 4, 4, A, 1.0, A, A, A,
+    ok = [A, pq2.PQ2_BF16, 512, 512, 128, 9, 1, 4, ctypes.addressof(c), A, 4, 4, A, 1.0, A, A, A,
           1 << 40, A, None]
     refused(L.pq2_attn_decode, ok, (0, None, NULL), (9, None, NULL), (12, None, NULL),
             (14, None, NULL), (16, None, NULL), (1, pq2.PQ2_F32, DTYPE), (1, 7, DTYPE),
@@ -91,9 +101,11 @@ def test_decode_refusals(L):
             (0, A + 2, ALIGN), (14, A + 8, ALIGN), (15, A + 2, ALIGN), (16, A + 8, ALIGN),
             (18, A + 1, ALIGN))
     f = L.pq2_attn_decode_workspace_bytes
-    assert f(1, 1, 4, 2, 128) > 0
-    for bad in ((0, 1, 4, 2, 128), (1, 0, 4, 2, 128), (1, 1, 3, 2, 128), (1, 1, 4, 2, 80),
-                (1, 1, 514, 2, 64)):
+    assert f(1, 1, 4, 2, 128, 4096) == 0 and f(16, 1, 8, 1, 128, 4096) == 0
+    for some in ((1, 1, 4, 2, 128, 4112), (17, 1, 8, 1, 64, 16), (1, 5, 320, 8, 64, 16)):
+        assert f(*some) > 0
+    for bad in ((0, 1, 4, 2, 128, 1 << 20), (1, 0, 4, 2, 128, 1 << 20), (1, 1, 3, 2, 128, 1 << 20),
+                (1, 1, 4, 2, 80, 1 << 20), (1, 1, 514, 2, 64, 1 << 20), (99, 1, 4, 2, 128, -1)):
         assert f(*bad) == 0
 
 

@@ -265,13 +265,29 @@ def test_offsets_beyond_32_bits():
 
 
 def test_a_workspace_of_the_callers():
-    lens = [1500, 2]
+    lens = [4500, 2]
     cache, table, dense = A.make_cache(2, lens, 2, 16, 128, F16, seed=2)
     q = queries(2, 1, 10, 128, F16, seed=1)
-    nbytes = pq2.lib().pq2_attn_decode_workspace_bytes(2, 1, 10, 2, 128)
-    space, back, guard = U.guarded((nbytes,), torch.uint8)
+    nbytes = pq2.lib().pq2_attn_decode_workspace_bytes(2, 1, 10, 2, 128, 16 * table.shape[1])
     back = torch.full((nbytes + 512,), 0x5A, dtype=torch.uint8, device="cuda")
     check(q, cache, table, lens, dense, workspace=back[256:256 + nbytes])
     assert bool((back[:256] == 0x5A).all()) and bool((back[256 + nbytes:] == 0x5A).all())
     with pytest.raises(pq2.Pq2Error):
         pq2.pq2_attn_decode(q, cache, table, ints(lens), workspace=back[256:256 + nbytes - 16])
+
+
+@pytest.mark.parametrize("dtype,cache_dtype", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,H,G,T", [([4096], 8, 5, 1), ([4000, 0, 1, 700], 4, 3, 1),
+                                        ([1, 2, 3, 2000, 513], 3, 6, 4), ([1025], 1, 8, 7)])
+def test_a_wider_table_changes_nothing(dtype, cache_dtype, D, lens, H, G, T):
+    """Short tables run in clusters, longer ones in even shares of the SMs: both
+    against 64 bits, and within two roundings of each other."""
+    B = len(lens)
+    cache, table, dense = A.make_cache(B, lens, H, 32, D, cache_dtype, seed=D + T, width=128)
+    q = queries(B, T, H * G, D, dtype, seed=4)
+    wide = torch.full((B, 200), -3, dtype=torch.int32, device="cuda")
+    wide[:, :128] = table
+    a = check(q, cache, table, lens, dense)
+    b = check(q, cache, wide, lens, dense)
+    assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -6 * float(a.float().abs().max())
