@@ -1,1041 +1,16 @@
-// pq2_attn_decode.cu — attention of the newest tokens over a paged cache.
-//
-// Per row (a token's query head), with scores s_j = c q . k_j (c = scale /
-// ln 2) over the positions that it sees, out = sum 2^(s_j - m) v_j / sum
-// 2^(s_j - m), m a running maximum of the scores seen so far, or at most 8
-// below it.
-//
-// Bound: HBM, the cache is read once.  The T * G rows of the query heads that
-// share a key head make one tile of 16 (more rows: several tiles, which read
-// the cache through L2), so every key and value is used for all of them: the
-// products are m16n8k16 MMAs, which at 16 rows need a third of the time that
-// the bytes take.
-//
-// Work is cut evenly whatever the lengths: the tiles of 16 * warps tokens of
-// all (sequence, key head, row tile) are numbered, and a CTA takes a
-// contiguous share of them, which may end inside a sequence and span several.
-// Inside a tile each warp has 16 tokens of its own, which it copies itself
-// (tensor-map boxes of 16 slots into a ring that no other warp touches, so
-// nothing waits for another warp before the join) and folds into sums of its
-// own.  At the end of a CTA's part of a sequence the warps join; parts that
-// are not whole go to the workspace, and a second kernel joins them.
-//
-// 8-bit caches: codes become fp16 by byte permutes (0x6400 | code + 128 is
-// 1024 + 128 + code) and one exact subtraction.  A key's scale multiplies its
-// score; a value's goes into its weight, w_j = 2^(s_j + log2 scale_j - m2)
-// with a maximum m2 of its own, so that weights are at most 2^8 and keep their
-// bits whatever the scales are.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <algorithm>
-#include <cmath>
-
-#include "pq2_internal.h"
-#include "pq2_tensor.cuh"
+// pq2_attn_decode.cu — attention of the newest tokens over a paged cache
+// (pq2_attn_decode.cuh): workspace, choice of the kernel, and the kernels over
+// 16-bit caches (pq2_attn_decode8.cu has those over 8-bit ones; two units only
+// for the time that they take to compile).
+#include "pq2_attn_decode.cuh"
 
 namespace pq2 {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;   // how far m may stay behind, in powers of two
-constexpr int kRows = 16;       // rows of an MMA tile
-constexpr int kJoinCols = 32;   // columns that the warps join at a time
-constexpr int kJoinStride = kJoinCols + 8;  // floats: rows land on other banks
-constexpr int kMaxCtas = 160;   // the SMs of the largest sm_103 device
-// Few items in short contexts: a cluster of 8 CTAs takes each and joins its
-// parts through distributed shared memory.  One launch and no workspace, which
-// at 1 x 1024 tokens, 8 key heads of 128 is @ against @ us; but a whole SM more or
-// less for 16 clusters is all that it can balance, so not beyond 16 items and
-// 4096 positions.
-constexpr int kCluster = 8, kClusterItems = 16, kClusterPositions = 4096;
-constexpr int kScaleBytes = 128;  // of 16 scales: a copy's target is 128-byte aligned
-
-// RT: row tiles of a CTA.  Its warps are RT x slices: the warps of one slice
-// share the slice's ring.
-template <typename CT, int D, int RT>
-struct Geo {
-  static constexpr bool eight = sizeof(CT) == 1;
-  static constexpr int warps = eight && D <= 128 ? 12 : 8, slices = warps / RT;
-  static constexpr int threads = warps * 32;
-  // Tokens of a slice: 32 codes share the steps between the MMAs; 16 elements
-  // of 16 bits leave that off the critical path and cut short contexts finer.
-  static constexpr int boxes16 = eight ? 2 : 1, tokens = 16 * boxes16;
-  static constexpr int tile = slices * tokens;      // tokens that a CTA takes at a time
-  static constexpr int rowBytes = D * (int)sizeof(CT);
-  static constexpr int boxBytes = rowBytes < 128 ? rowBytes : 128;
-  static constexpr int boxes = rowBytes / boxBytes;  // of 16 tokens
-  static constexpr int sixteen = 16 * rowBytes;      // bytes of 16 tokens
-  static constexpr int unit = boxes16 * sixteen;     // a slice's K, or its V
-  static constexpr int rows = RT * kRows;
-  static constexpr int joinBytes = warps * kRows * kJoinStride * 4;
-  static constexpr int qBytes = RT * (D / 16) * 512;
-  static constexpr int statBytes = 3 * warps * kRows * 4;
-  // What beginning an item costs (its queries, the join), in tiles: about the
-  // time of 96 KB (measured @).
-  static constexpr int begin = (98304 + tile * rowBytes * 2 - 1) / (tile * rowBytes * 2);
-  static constexpr int scale = eight ? boxes16 * kScaleBytes : 0;  // of a unit
-  static constexpr int depth =
-      std::min(8, (227 * 1024 - 1024 - 1024 - joinBytes - qBytes - statBytes) /
-                      ((unit + scale) * slices));
-  static constexpr int offScale = slices * depth * unit;
-  static constexpr int offJoin = offScale + slices * depth * scale;
-  static constexpr int offQ = offJoin + joinBytes;
-  static constexpr int offStat = offQ + qBytes;       // [3][warps][16]
-  static constexpr int offBar = offStat + statBytes;
-  static constexpr int smem = offBar + 2 * slices * depth * 8 + 1024;
-  static_assert(smem <= 227 * 1024 && depth >= 2, "shared memory");
-  static constexpr int slot = rows * D + 3 * rows;  // floats of a part in the workspace
-};
-
-struct Params {
-  DecodeParams a;
-  pq2_kv_cache cache;
-  int group, rows, row_groups, items;  // G, T * G, groups of RT tiles, heads * row_groups
-  float c;
-  float* parts;   // [2 * CTAs][slot]
-  int4* places;   // [CTAs]: sequence, item, first CTA, number of parts (0: nothing to join)
-  int cluster;    // CTAs that share an item and join it themselves; 0: even shares
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// 2^(m - top), 0 for the maximum of nothing.
-__device__ __forceinline__ float weight(float m, float top) {
-  return m == -INFINITY ? 0.f : ex2(m - top);
-}
-
-template <typename T> __device__ __forceinline__ uint32_t pack(float lo, float hi);
-template <> __device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float widen(int8_t x) { return (float)x; }
-
-template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint4& a, uint32_t b0,
-                                            uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint4& a, uint32_t b0,
-                                                   uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 ldsm(uint32_t addr) {
-  uint4 r;
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(addr)
-               : "memory");
-  return r;
-}
-__device__ __forceinline__ uint4 ldsm_t(uint32_t addr) {
-  uint4 r;
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(addr)
-               : "memory");
-  return r;
-}
-// Codes x and y (bytes X and Y of u, already 128 above) as fp16 pairs.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes(uint32_t u) {
-  const uint32_t h = __byte_perm(u, 0x64646464u, SEL);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                            __half2half2(__ushort_as_half(0x6480)));  // 1152
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                       int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                       uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-// An address of this CTA's shared memory in the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t map_rank(const void* p, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float remote(uint32_t addr) {
-  float r;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ float4 remote4(uint32_t addr) {
-  float4 r;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-               : "r"(addr));
-  return r;
-}
-
-__device__ __forceinline__ int length(const Params& p, int b) {
-  return b < p.a.batch.B ? max(__ldg(p.a.batch.lens + b), 0) : 0;
-}
-__device__ __forceinline__ int tiles_of(int len, int tile) {
-  return max(1, len / tile + (len % tile != 0));
-}
-
-// Where a CTA, or one of its warps' copies, is in the CTA's share.
-struct Cursor {
-  int b, head, group, tile, tiles, len, next_len, left;
-};
-template <int TILE, int BEGIN>
-__device__ __forceinline__ void next_tile(Cursor& c, const Params& p) {
-  --c.left;
-  if (++c.tile < c.tiles) return;
-  c.tile = 0, c.left -= BEGIN;
-  if (++c.group < p.row_groups) return;
-  c.group = 0;
-  if (++c.head < (int)p.cache.heads) return;
-  c.head = 0, ++c.b;
-  c.len = c.next_len;
-  c.tiles = tiles_of(c.len, TILE);
-  c.next_len = length(p, c.b + 1);
-}
-
-// Four columns of one row by the formula itself, for rows whose sums met an
-// infinity or NaN although they do not see the newest positions: an MMA
-// multiplies every value of a slice by its weight, and 0 * NaN would stay.
-template <typename QT, typename CT, int D>
-__device__ __noinline__ float4 plain_columns(const Params& p, int b, int kh, int R, int d,
-                                             int most, float m, float l) {
-  const QT* q = static_cast<const QT*>(p.a.q) + b * p.a.batch_stride +
-                R / p.group * p.a.token_stride + (kh * p.group + R % p.group) * p.a.head_stride;
-  float o[4] = {};
-#pragma unroll 1
-  for (int j = 0; j < most; ++j) {
-    const int64_t at = j / p.cache.page_size, slot = j - at * p.cache.page_size;
-    const int64_t page =
-        at < p.a.batch.table_width ? __ldg(p.a.batch.table + b * p.a.batch.table_stride + at) : -1;
-    const bool there = page >= 0 && page < p.cache.pages;
-    const int64_t from =
-        page * p.cache.page_stride + kh * p.cache.head_stride + slot * p.cache.token_stride;
-    const int64_t side = (page * p.cache.heads + kh) * p.cache.page_size + slot;
-    float s = 0.f;
-    if (there) {
-      const CT* k = static_cast<const CT*>(p.cache.k) + from;
-#pragma unroll 4
-      for (int i = 0; i < D; ++i) s = fmaf(widen(q[i]), widen(k[i]), s);
-      if (sizeof(CT) == 1) s *= p.cache.k_scales[side];
-    }
-    const float w = ex2(fmaf(s, p.c, -m));
-    if (there) {
-      const CT* v = static_cast<const CT*>(p.cache.v) + from + d;
-      const float vs = sizeof(CT) == 1 ? p.cache.v_scales[side] : 1.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(w, widen(v[i]) * vs, o[i]);
-    }
-  }
-  return make_float4(o[0] / l, o[1] / l, o[2] / l, o[3] / l);
-}
-
-// Four columns of a joined row to out, and its lse: o in units of 2^m2, the
-// weights' sum l in units of 2^m.
-template <typename QT, typename CT, int D>
-__device__ __forceinline__ void finish(const Params& p, int b, int kh, int R, int d, int len,
-                                       float4 o, float m, float l, float m2) {
-  if (R >= p.rows) return;
-  const int t = R / p.group, most = len - p.a.T + t + 1;
-  const int64_t row =
-      ((int64_t)b * p.a.T + t) * p.a.q_heads + kh * p.group + R % p.group;
-  if (most <= 0) {
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-  } else {
-    const float f = (sizeof(CT) == 1 ? weight(m2, m) : 1.f) / l;
-    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-    const float zero = (o.x + o.y) * 0.f + (o.z + o.w) * 0.f;
-    if (zero != 0.f && l - l == 0.f && most < len)
-      o = plain_columns<QT, CT, D>(p, b, kh, R, d, most, m, l);
-  }
-  *reinterpret_cast<uint2*>(static_cast<QT*>(p.a.out) + row * D + d) =
-      make_uint2(pack<QT>(o.x, o.y), pack<QT>(o.z, o.w));
-  if (d == 0 && p.a.lse) p.a.lse[row] = most > 0 ? m * kLn2 + logf(l) : -INFINITY;
-}
-
-template <typename QT, typename CT, int D, int RT>
-__global__ void __launch_bounds__(Geo<CT, D, RT>::threads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v,
-                  const __grid_constant__ CUtensorMap map_ks,
-                  const __grid_constant__ CUtensorMap map_vs, const Params p) {
-  using G = Geo<CT, D, RT>;
-  constexpr int W = G::warps, kTile = G::tile, kTokens = G::tokens, NT = kTokens / 8;
-  constexpr bool kEight = G::eight;
-  using MT = typename std::conditional<kEight, __half, QT>::type;  // the MMAs' type
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw_s = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
-  float* join = reinterpret_cast<float*>(smem + G::offJoin);
-  uint4* q_frag = reinterpret_cast<uint4*>(smem + G::offQ);
-  float* stat = reinterpret_cast<float*>(smem + G::offStat);  // m, l, m2 of [warp][row]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::offBar);
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, i4 = lane & 3;  // fragment row and column pair
-  const int slice = warp % G::slices, rt = warp / G::slices;
-  uint64_t* bar = bars + slice * G::depth;           // a unit has arrived
-  uint64_t* freed = bar + G::slices * G::depth;      // all row tiles have read it
-  if (rt == 0 && lane == 0) {
-    for (int i = 0; i < G::depth; ++i) mbar_init(&bar[i], 1), mbar_init(&freed[i], RT);
-    fence_barrier_init();
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // The CTA's share: the tiles of all items are counted, with G::begin more in
-  // front of each item's, then the sequence that holds the first of the share
-  // is found.
-  Cursor here;
-  int parts = 1, rank = 0;  // of a cluster's item
-  if (p.cluster) {
-    const int of = blockIdx.x / kCluster;
-    rank = blockIdx.x % kCluster;
-    here.b = of / p.items;
-    here.head = of % p.items / p.row_groups, here.group = of % p.items % p.row_groups;
-    here.len = length(p, here.b), here.next_len = 0;
-    here.tiles = tiles_of(here.len, kTile);
-    parts = min(here.tiles, kCluster);
-    here.tile = rank < parts ? (int)((int64_t)rank * here.tiles / parts) : 0;
-    here.left = rank < parts ? (int)((int64_t)(rank + 1) * here.tiles / parts) - here.tile : 0;
-    __syncthreads();
-  } else {
-    uint64_t* sums = reinterpret_cast<uint64_t*>(join);   // [W], then the place
-    int* place = reinterpret_cast<int*>(sums + W);
-    uint64_t total = 0;
-    for (int b = tid; b < p.a.batch.B; b += G::threads) total += tiles_of(length(p, b), kTile) + G::begin;
-#pragma unroll
-    for (int o = 16; o; o /= 2) total += __shfl_xor_sync(~0u, total, o);
-    if (lane == 0) sums[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) total += sums[w];
-    total *= p.items;
-    const uint64_t ctas = min((uint64_t)gridDim.x, total), c = blockIdx.x;
-    if (c >= ctas) {
-      if (tid == 0) p.places[c] = make_int4(0, 0, 0, 0);
-      return;
-    }
-    const uint64_t t0 = c * total / ctas, t1 = (c + 1) * total / ctas;
-    uint64_t before = 0;
-    for (int b0 = 0; b0 < p.a.batch.B; b0 += G::threads) {
-      const int b = b0 + tid;
-      const uint64_t n =
-          b < p.a.batch.B ? (uint64_t)(tiles_of(length(p, b), kTile) + G::begin) * p.items : 0;
-      uint64_t upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const uint64_t x = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += x;
-      }
-      __syncthreads();
-      if (lane == 31) sums[warp] = upto;
-      __syncthreads();
-      uint64_t sum = before;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w < warp) upto += sums[w];
-        sum += sums[w];
-      }
-      upto += before;
-      if (t0 >= upto - n && t0 < upto) {
-        const uint64_t in = t0 - (upto - n);
-        const int tiles = (int)(n / p.items);
-        place[0] = b, place[1] = (int)(in / tiles), place[2] = (int)(in % tiles);
-      }
-      before = sum;
-      if (t0 < sum) break;
-    }
-    __syncthreads();
-    const int in = place[2];  // place in the item
-    here.b = place[0], here.tile = max(in - G::begin, 0);
-    here.head = place[1] / p.row_groups, here.group = place[1] % p.row_groups;
-    here.len = length(p, here.b), here.next_len = length(p, here.b + 1);
-    here.tiles = tiles_of(here.len, kTile);
-    here.left = (int)(t1 - t0) - max(G::begin - in, 0);
-    // If the share begins inside an item, and no share before it does, the
-    // second kernel's CTA of this number joins that item.
-    if (tid == 0) {
-      int4 to = make_int4(0, 0, 0, 0);
-      if (here.tile > 0) {
-        const uint64_t a = t0 - here.tile, z = a + here.tiles - 1;
-        const uint64_t c0 = ((a + 1) * ctas - 1) / total, c1 = ((z + 1) * ctas - 1) / total;
-        if (c0 + 1 == c) to = make_int4(here.b, place[1], (int)c0, (int)(c1 - c0 + 1));
-      }
-      p.places[c] = to;
-    }
-    __syncthreads();
-  }
-
-  // ------------------------------------------------------------- the copies
-  bool ok = true;
-  uint8_t* ring_p = smem + slice * (G::depth * G::unit);
-  const uint32_t ring = smem_u32(ring_p);
-  uint8_t* scale_p = smem + G::offScale + slice * (G::depth * G::scale);
-  Cursor copy = here;
-  uint32_t issued = 0, used = 0;  // units: K and V of a slice in turn
-  // Lane i: page and slot of 16 tokens, those of the slice in the tiles from
-  // pages_tile on, in order.
-  constexpr int kAhead = 32 / G::boxes16;
-  int pages = 0, slots = 0, pages_b = -1, pages_tile = 0;
-  // To the slice's next tile that holds a token.
-  const auto seek = [&]() {
-    while (copy.left > 0 && copy.tile * kTile + slice * kTokens >= copy.len)
-      next_tile<kTile, G::begin>(copy, p);
-    if (copy.left > 0 && (copy.b != pages_b || copy.tile < pages_tile ||
-                          copy.tile >= pages_tile + kAhead)) {
-      pages_b = copy.b, pages_tile = copy.tile;
-      const int page_size = (int)p.cache.page_size, tile = copy.tile + lane / G::boxes16;
-      pages = -1, slots = 0;
-      if (tile < copy.tiles) {
-        const int token = tile * kTile + slice * kTokens + lane % G::boxes16 * 16;
-        const int at = token / page_size;
-        slots = token - at * page_size;
-        if (at < p.a.batch.table_width)
-          pages = __ldg(p.a.batch.table + copy.b * p.a.batch.table_stride + at);
-      }
-    }
-  };
-  // The next unit's copies; for several row tiles the first one's warp makes
-  // them when all have read what the ring holds there.
-  const auto issue = [&]() {
-    if (copy.left <= 0) return;
-    const uint32_t st = issued % G::depth;
-    if (RT > 1 && rt == 0 && issued >= G::depth)
-      ok = ok && mbar_wait(&freed[st], issued / G::depth - 1 & 1);
-    const int from = (copy.tile - pages_tile) * G::boxes16;
-    int page[G::boxes16], slot[G::boxes16];
-#pragma unroll
-    for (int k = 0; k < G::boxes16; ++k) {
-      page[k] = __shfl_sync(~0u, pages, from + k);
-      slot[k] = __shfl_sync(~0u, slots, from + k);
-    }
-    if (rt == 0 && lane == 0) {
-      const bool values = issued & 1;
-      const uint32_t mb = smem_u32(&bar[st]);
-      mbar_arrive_expect_tx(&bar[st], G::unit + (kEight ? kTokens * 4 : 0));
-#pragma unroll
-      for (int k = 0; k < G::boxes16; ++k) {
-#pragma unroll
-        for (int x = 0; x < G::boxes; ++x)
-          tma_4d(ring + st * G::unit + k * G::sixteen + x * (16 * G::boxBytes),
-                 values ? &map_v : &map_k, x * (G::boxBytes / (int)sizeof(CT)), slot[k], copy.head,
-                 page[k], mb);
-        if (kEight)
-          tma_3d(smem_u32(scale_p) + st * G::scale + k * kScaleBytes, values ? &map_vs : &map_ks,
-                 slot[k], copy.head, page[k], mb);
-      }
-    }
-    if (issued & 1) {
-      next_tile<kTile, G::begin>(copy, p);
-      seek();
-    }
-    ++issued;
-  };
-  // The warp has read the unit in use.
-  const auto release = [&]() {
-    __syncwarp();
-    if (RT > 1) warp_arrive(&freed[used % G::depth]);
-    issue();
-    ++used;
-  };
-  seek();
-#pragma unroll 1
-  for (int i = 0; i < G::depth; ++i) issue();
-
-  // Lane addresses inside a unit.  16 bits: an MMA's K fragments are tokens 0-7
-  // and 8-15 x columns 0-7 and 8-15; V's are read transposed.  8 bits: 16 codes
-  // of a token are one row of a matrix, for both.  Pieces of 16 bytes are
-  // swizzled as the copies left them.
-  const int tk = kEight ? (lane & 7) + (lane >> 3 & 1) * 8 : (lane & 7) + (lane >> 4) * 8;
-  const int tv = (lane & 7) + (lane >> 3 & 1) * 8;
-  const auto lane_base = [&](int token, int piece) {
-    const int turn = G::boxBytes == 128 ? token & 7 : token >> 1 & 3;
-    return (uint32_t)(token * G::boxBytes + ((piece ^ turn) << 4));
-  };
-  const uint32_t at_k = lane_base(tk, kEight ? lane >> 4 : lane >> 3 & 1);
-  const uint32_t at_v = lane_base(tv, lane >> 4);
-  // The lane's piece pair i of 16 tokens.
-  const auto piece = [&](uint32_t base, uint32_t at, int i) {
-    constexpr int kPairs = G::boxBytes / 32;
-    return base + i / kPairs * (16 * G::boxBytes) + (at ^ (i % kPairs << 5));
-  };
-
-  // ------------------------------------------------------- the rows' queries
-  // A fragments: row g (and g + 8), columns of step i: 16 bits 16 i + 2 i4 +
-  // {0, 1, 8, 9}; 8 bits 16 i + 4 i4 + {0 .. 3}, the order of a code word.
-  const auto fetch_q = [&](const Cursor& at) {
-    for (int f = tid; f < RT * (D / 16) * 32; f += G::threads) {
-      const int fl = f & 31, step = (f >> 5) % (D / 16), row0 = f / (D / 16 * 32) * kRows + (fl >> 2);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int R = at.group * G::rows + row0 + 8 * half;
-        const QT* q = static_cast<const QT*>(p.a.q);
-        if (R < p.rows)
-          q += at.b * p.a.batch_stride + R / p.group * p.a.token_stride +
-               (at.head * p.group + R % p.group) * p.a.head_stride + step * 16 +
-               (fl & 3) * (kEight ? 4 : 2);
-        const uint32_t to = smem_u32(q_frag + f) + 4 * half;
-        const uint32_t bytes = R < p.rows ? 4 : 0;  // rows behind the last one: zeros
-        asm volatile(
-            "cp.async.ca.shared.global [%0], [%2], 4, %4;\n\t"
-            "cp.async.ca.shared.global [%1], [%3], 4, %4;" ::"r"(to), "r"(to + 8), "l"(q),
-            "l"(q + (R < p.rows ? (kEight ? 2 : 8) : 0)), "r"(bytes)
-            : "memory");
-      }
-    }
-  };
-  if (here.left > 0) fetch_q(here);
-
-  while (here.left > 0) {
-    const int first = here.tile, last = min(here.tiles, here.tile + here.left);
-    const int b = here.b, head = here.head, len = here.len, R0 = here.group * G::rows;
-    const bool whole = first == 0 && last == here.tiles;
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    const int r0 = rt * kRows + g, r1 = r0 + 8;  // the thread's rows
-    const uint4* mine_q = q_frag + rt * (D / 16 * 32) + lane;
-    float c0 = p.c, c1 = p.c;
-    if constexpr (kEight && !std::is_same<QT, __half>::value) {
-      // bf16 queries as fp16: scaled by a power of two so that the row's
-      // largest lies in [2^14, 2^15); what fp16 loses lies 2^-39 below that.
-      uint32_t top0 = 0, top1 = 0;  // pairs of magnitudes
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint4 a = mine_q[i * 32];
-        top0 = __vmaxu2(top0, __vmaxu2(a.x & 0x7FFF7FFFu, a.z & 0x7FFF7FFFu));
-        top1 = __vmaxu2(top1, __vmaxu2(a.y & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
-      }
-#pragma unroll
-      for (int x = 1; x < 4; x *= 2) {
-        top0 = __vmaxu2(top0, __shfl_xor_sync(~0u, top0, x));
-        top1 = __vmaxu2(top1, __shfl_xor_sync(~0u, top1, x));
-      }
-      // The scale's exponent; that of 1 for rows of zeros or infinities.
-      const auto scale_of = [](uint32_t top) {
-        const int e = (int)(max(top & 0xFFFFu, top >> 16) >> 7);
-        return e == 0 || e == 255 ? 127 : min(max(268 - e, 1), 253);
-      };
-      const int up0 = scale_of(top0), up1 = scale_of(top1);
-      const float s0 = __uint_as_float((uint32_t)up0 << 23), s1 = __uint_as_float((uint32_t)up1 << 23);
-      c0 *= __uint_as_float((uint32_t)(254 - up0) << 23);
-      c1 *= __uint_as_float((uint32_t)(254 - up1) << 23);
-      const auto scaled = [](uint32_t x, float by) {
-        return pack<__half>(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xFFFF0000u) * by);
-      };
-      __syncthreads();
-      uint4* out_q = q_frag + rt * (D / 16 * 32) + lane;
-      for (int i = slice; i < D / 16; i += G::slices) {
-        const uint4 a = out_q[i * 32];
-        out_q[i * 32] = make_uint4(scaled(a.x, s0), scaled(a.y, s1), scaled(a.z, s0), scaled(a.w, s1));
-      }
-      __syncthreads();
-    }
-    // How many positions they see.
-    const int most0 = len - p.a.T + (R0 + r0) / p.group + 1;
-    const int most1 = len - p.a.T + (R0 + r1) / p.group + 1;
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    // 8-bit caches: m2, and 2^(m - m2).
-    float n0 = -INFINITY, n1 = -INFINITY, e0 = 1.f, e1 = 1.f;
-#pragma unroll 1
-    for (int tile = first; tile < last; ++tile) {
-      const int token = tile * kTile + slice * kTokens;
-      if (token >= len) continue;
-      // ------------------------------------------------------------- scores
-      uint32_t st = used % G::depth;
-      ok = ok && mbar_wait(&bar[st], used / G::depth & 1);
-      uint32_t from = ring + st * G::unit;
-      const float* scales = reinterpret_cast<const float*>(scale_p + st * G::scale) + 2 * i4;
-      float s[NT][4] = {};  // tokens 8 n .. 8 n + 7
-      if constexpr (kEight) {
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 qa = mine_q[(2 * i) * 32], qb = mine_q[(2 * i + 1) * 32];
-#pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            uint4 k = ldsm(piece(from + n / 2 * G::sixteen, at_k, i));
-            k.x ^= 0x80808080u, k.y ^= 0x80808080u, k.z ^= 0x80808080u, k.w ^= 0x80808080u;
-            mma<MT>(s[n], qa, codes<0x4140>(k.x), codes<0x4342>(k.x));
-            mma<MT>(s[n + 1], qa, codes<0x4140>(k.y), codes<0x4342>(k.y));
-            mma<MT>(s[n], qb, codes<0x4140>(k.z), codes<0x4342>(k.z));
-            mma<MT>(s[n + 1], qb, codes<0x4140>(k.w), codes<0x4342>(k.w));
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 k = *reinterpret_cast<const float2*>(scales + n / 2 * (kScaleBytes / 4) +
-                                                            n % 2 * 8);
-          s[n][0] *= k.x * c0, s[n][1] *= k.y * c0, s[n][2] *= k.x * c1, s[n][3] *= k.y * c1;
-        }
-      } else {
-        // Two sums of every score: a chain of MMAs half as long.
-        float s2[NT][4] = {};
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 qa = mine_q[i * 32];
-#pragma unroll
-          for (int n = 0; n < NT; n += 2) {
-            const uint4 k = ldsm(piece(from + n / 2 * G::sixteen, at_k, i));
-            mma<MT>(i & 1 ? s2[n] : s[n], qa, k.x, k.y);
-            mma<MT>(i & 1 ? s2[n + 1] : s[n + 1], qa, k.z, k.w);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s[n][0] = (s[n][0] + s2[n][0]) * c0, s[n][1] = (s[n][1] + s2[n][1]) * c0;
-          s[n][2] = (s[n][2] + s2[n][2]) * c1, s[n][3] = (s[n][3] + s2[n][3]) * c1;
-        }
-      }
-      release();
-      const bool edge = token + kTokens > len - p.a.T + 1;  // some row does not see all
-      if (edge) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = token + 8 * n + 2 * i4 + e;
-            if (j >= most0) s[n][e] = -INFINITY;
-            if (j >= most1) s[n][2 + e] = -INFINITY;
-          }
-      }
-      // ------------------------------------------------------------ weights
-      // The rows' maximum is only put together when a lane's is over the slack.
-      float h0 = fmaxf(s[0][0], s[0][1]), h1 = fmaxf(s[0][2], s[0][3]);
-#pragma unroll
-      for (int n = 1; n < NT; ++n) {
-        h0 = fmaxf(h0, fmaxf(s[n][0], s[n][1]));
-        h1 = fmaxf(h1, fmaxf(s[n][2], s[n][3]));
-      }
-      if (__any_sync(~0u, h0 - m0 > kSlack || h1 - m1 > kSlack)) {
-        h0 = fmaxf(h0, __shfl_xor_sync(~0u, h0, 1)), h1 = fmaxf(h1, __shfl_xor_sync(~0u, h1, 1));
-        h0 = fmaxf(h0, __shfl_xor_sync(~0u, h0, 2)), h1 = fmaxf(h1, __shfl_xor_sync(~0u, h1, 2));
-        h0 = fmaxf(h0, m0), h1 = fmaxf(h1, m1);
-        const float f0 = weight(m0, h0), f1 = weight(m1, h1);
-        m0 = h0, m1 = h1;
-        l0 *= f0, l1 *= f1;
-        if constexpr (kEight) {
-          if (n0 != -INFINITY) e0 = ex2(fminf(m0 - n0, 126.f));
-          if (n1 != -INFINITY) e1 = ex2(fminf(m1 - n1, 126.f));
-        } else {
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
-        }
-      }
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        s[n][0] = ex2(s[n][0] - z0), s[n][1] = ex2(s[n][1] - z0);
-        s[n][2] = ex2(s[n][2] - z1), s[n][3] = ex2(s[n][3] - z1);
-        l0 += s[n][0] + s[n][1], l1 += s[n][2] + s[n][3];
-      }
-      st = used % G::depth;
-      ok = ok && mbar_wait(&bar[st], used / G::depth & 1);
-      from = ring + st * G::unit;
-      if constexpr (kEight) {
-        // The same with the values' scales in the weights: 2^(s - m) v 2^(m - m2).
-        scales = reinterpret_cast<const float*>(scale_p + st * G::scale) + 2 * i4;
-        h0 = 0.f, h1 = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float2 v = *reinterpret_cast<const float2*>(scales + n / 2 * (kScaleBytes / 4) +
-                                                      n % 2 * 8);
-          s[n][0] *= v.x * e0, s[n][1] *= v.y * e0, s[n][2] *= v.x * e1, s[n][3] *= v.y * e1;
-          if (edge) {
-            // What a row does not see may have any scale.
-            const int j = token + 8 * n + 2 * i4;
-            if (j >= most0) s[n][0] = 0.f;
-            if (j + 1 >= most0) s[n][1] = 0.f;
-            if (j >= most1) s[n][2] = 0.f;
-            if (j + 1 >= most1) s[n][3] = 0.f;
-          }
-          h0 = fmaxf(h0, fmaxf(s[n][0], s[n][1])), h1 = fmaxf(h1, fmaxf(s[n][2], s[n][3]));
-        }
-        constexpr float kMost = 256.f;  // 2^kSlack
-        if (__any_sync(~0u, h0 > kMost || h1 > kMost || n0 == -INFINITY || n1 == -INFINITY)) {
-          h0 = fmaxf(h0, __shfl_xor_sync(~0u, h0, 1)), h1 = fmaxf(h1, __shfl_xor_sync(~0u, h1, 1));
-          h0 = fmaxf(h0, __shfl_xor_sync(~0u, h0, 2)), h1 = fmaxf(h1, __shfl_xor_sync(~0u, h1, 2));
-          // Without an m2 yet the weights are in units of 2^m.
-          const bool up0 = h0 > (n0 == -INFINITY ? 0.f : kMost);
-          const bool up1 = h1 > (n1 == -INFINITY ? 0.f : kMost);
-          const float k0 = up0 ? lg2(h0) : 0.f, k1 = up1 ? lg2(h1) : 0.f;
-          if (up0) n0 = (n0 == -INFINITY ? m0 : n0) + k0, e0 = ex2(fminf(m0 - n0, 126.f));
-          if (up1) n1 = (n1 == -INFINITY ? m1 : n1) + k1, e1 = ex2(fminf(m1 - n1, 126.f));
-          const float f0 = ex2(-k0), f1 = ex2(-k1);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) s[n][0] *= f0, s[n][1] *= f0, s[n][2] *= f1, s[n][3] *= f1;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
-        }
-      } else if (token + kTokens > len) {
-        // Slots behind the last position hold anything: zeros, so that a weight
-        // of zero times them is zero.
-        if (rt == 0) {
-          for (int x = lane; x < G::unit / 16; x += 32)
-            if (x / (G::sixteen / 16) * 16 + (x >> 3) % 16 >= len - token)
-              *reinterpret_cast<uint4*>(ring_p + st * G::unit + x * 16) = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        if (RT > 1) named_bar_sync(1 + slice, RT * 32);
-        __syncwarp();
-      }
-      // ------------------------------------------------------------ products
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        const uint4 a = make_uint4(pack<MT>(s[n][0], s[n][1]), pack<MT>(s[n][2], s[n][3]),
-                                   pack<MT>(s[n + 1][0], s[n + 1][1]),
-                                   pack<MT>(s[n + 1][2], s[n + 1][3]));
-        if constexpr (kEight) {
-          // Columns 16 i + 4 i4 + {0, 2} in o[2 i], {1, 3} in o[2 i + 1].
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint4 v = ldsm_t(piece(from + n / 2 * G::sixteen, at_v, i));
-            v.x ^= 0x80808080u, v.y ^= 0x80808080u, v.z ^= 0x80808080u, v.w ^= 0x80808080u;
-            mma<MT>(o[4 * i], a, codes<0x4240>(v.x), codes<0x4240>(v.y));
-            mma<MT>(o[4 * i + 1], a, codes<0x4341>(v.x), codes<0x4341>(v.y));
-            mma<MT>(o[4 * i + 2], a, codes<0x4240>(v.z), codes<0x4240>(v.w));
-            mma<MT>(o[4 * i + 3], a, codes<0x4341>(v.z), codes<0x4341>(v.w));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint4 v = ldsm_t(piece(from + n / 2 * G::sixteen, at_v, i));
-            mma<MT>(o[2 * i], a, v.x, v.y);
-            mma<MT>(o[2 * i + 1], a, v.z, v.w);
-          }
-        }
-      }
-      release();
-    }
-
-    // ----------------------------------------------------- the warps' join
-    l0 += __shfl_xor_sync(~0u, l0, 1), l1 += __shfl_xor_sync(~0u, l1, 1);
-    l0 += __shfl_xor_sync(~0u, l0, 2), l1 += __shfl_xor_sync(~0u, l1, 2);
-    if (i4 == 0) {
-      float* to = stat + warp * kRows;
-      to[g] = m0, to[g + 8] = m1;
-      to += W * kRows;
-      to[g] = l0, to[g + 8] = l1;
-      to += W * kRows;
-      to[g] = kEight ? n0 : m0, to[g + 8] = kEight ? n1 : m1;
-    }
-    // On to the next item: its queries come in while this one is joined.
-    here.left -= last - first - 1;
-    here.tile = last - 1;
-    next_tile<kTile, G::begin>(here, p);
-    // In a cluster the ring, which is empty now, takes the part.
-    float* part = p.cluster ? reinterpret_cast<float*>(smem)
-                            : p.parts + (size_t)(2 * blockIdx.x + (first == 0)) * G::slot;
-    // Thread (r, x): row r, columns 4 x of every round; its row tile's warps.
-    // With at most 8 rows the places of the rows behind them take the next
-    // block of columns, so that there are half as many rounds.
-    constexpr int S = G::slices, kRounds = D / kJoinCols;
-    const bool few = RT == 1 && p.rows <= 8;
-    const int place = tid >> 3, w0 = place / kRows * S;
-    const int r = few ? place & 7 : place;
-    const int x4 = (tid & 7) * 4 + (few ? place / 8 * kJoinCols : 0);
-    float M = -INFINITY, M2 = -INFINITY, L = 0.f, f[S];
-#pragma unroll
-    for (int round = 0; round < kRounds; ++round) {
-      if (few && (round & 1)) continue;
-      if (round) __syncthreads();
-      float* mine = join + warp * (kRows * kJoinStride);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float(&y)[4] = o[round * 4 + n];
-        const float(&next)[4] = o[(round + 1) % kRounds * 4 + n];
-        const float y2 = few ? next[0] : y[2], y3 = few ? next[1] : y[3];
-        if constexpr (kEight) {
-          const int col = n / 2 * 16 + 4 * i4 + (n & 1);
-          mine[g * kJoinStride + col] = y[0], mine[g * kJoinStride + col + 2] = y[1];
-          mine[(g + 8) * kJoinStride + col] = y2, mine[(g + 8) * kJoinStride + col + 2] = y3;
-        } else {
-          const int col = n * 8 + 2 * i4;
-          *reinterpret_cast<float2*>(mine + g * kJoinStride + col) = make_float2(y[0], y[1]);
-          *reinterpret_cast<float2*>(mine + (g + 8) * kJoinStride + col) = make_float2(y2, y3);
-        }
-      }
-      __syncthreads();
-      if (round == 0 && here.left > 0) fetch_q(here);
-      if (tid < G::rows * 8 && R0 + r < p.rows) {
-        const float* st = stat + w0 * kRows + r % kRows;
-        if (round == 0) {
-#pragma unroll
-          for (int w = 0; w < S; ++w) {
-            M = fmaxf(M, st[w * kRows]);
-            M2 = fmaxf(M2, st[(2 * W + w) * kRows]);
-          }
-#pragma unroll
-          for (int w = 0; w < S; ++w) {
-            L += st[(W + w) * kRows] * weight(st[w * kRows], M);
-            f[w] = weight(st[(2 * W + w) * kRows], M2);
-          }
-        }
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < S; ++w) {
-          const float4 y = *reinterpret_cast<const float4*>(
-              join + ((w0 + w) * kRows + place % kRows) * kJoinStride + (tid & 7) * 4);
-          sum.x = fmaf(y.x, f[w], sum.x), sum.y = fmaf(y.y, f[w], sum.y);
-          sum.z = fmaf(y.z, f[w], sum.z), sum.w = fmaf(y.w, f[w], sum.w);
-        }
-        const int d = round * kJoinCols + x4;
-        if (whole) {
-          finish<QT, CT, D>(p, b, head, R0 + r, d, len, sum, M, L, M2);
-        } else {
-          *reinterpret_cast<float4*>(part + r * D + d) = sum;
-          if (d == 0) {
-            part[G::rows * D + r] = M;
-            part[G::rows * D + G::rows + r] = L;
-            part[G::rows * D + 2 * G::rows + r] = M2;
-          }
-        }
-      }
-    }
-  }
-  if (p.cluster) {
-    cluster_sync();
-    if (parts > 1) {
-      const int of = blockIdx.x / kCluster, b = of / p.items;
-      const int head = of % p.items / p.row_groups, R0 = of % p.items % p.row_groups * G::rows;
-      const int valid = min(G::rows, p.rows - R0), len = length(p, b);
-      const float* part = reinterpret_cast<const float*>(smem);
-      for (int i = tid * kCluster + rank; i < valid * (D / 4); i += G::threads * kCluster) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float m[kCluster], l[kCluster], m2[kCluster];
-        float4 y[kCluster];
-        float M = -INFINITY, M2 = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int k = 0; k < kCluster; ++k) {
-          m[k] = m2[k] = -INFINITY, l[k] = 0.f, y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k < parts) {
-            const uint32_t at = map_rank(part, k), st = at + (G::rows * D + r) * 4;
-            m[k] = remote(st), l[k] = remote(st + G::rows * 4), m2[k] = remote(st + G::rows * 8);
-            y[k] = remote4(at + (r * D + d) * 4);
-          }
-          M = fmaxf(M, m[k]), M2 = fmaxf(M2, m2[k]);
-        }
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kCluster; ++k) {
-          L += l[k] * weight(m[k], M);
-          const float f = weight(m2[k], M2);
-          sum.x = fmaf(y[k].x, f, sum.x), sum.y = fmaf(y[k].y, f, sum.y);
-          sum.z = fmaf(y[k].z, f, sum.z), sum.w = fmaf(y[k].w, f, sum.w);
-        }
-        finish<QT, CT, D>(p, b, head, R0 + r, d, len, sum, M, L, M2);
-      }
-    }
-    cluster_sync();  // until all have read this CTA's part
-  }
-  if (!ok) report(p.a.status, PQ2_ERR_TIMEOUT);
-}
-
-// Joins the parts of one row: the CTA that began the item wrote its part into
-// its second slot, the ones after it into their first.
-template <typename QT, typename CT, int D, int RT>
-__global__ void __launch_bounds__(256) join_kernel(const Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  using G = Geo<CT, D, RT>;
-  constexpr int kCols = D / 4, kSplit = 256 / kCols;  // threads of a row, shares of the parts
-  __shared__ float4 sums[kSplit][kCols];
-  __shared__ float stats[kSplit][3];
-  const int4 to = p.places[blockIdx.x];
-  if (!to.w) return;
-  const int r = blockIdx.y, col = threadIdx.x % kCols, share = threadIdx.x / kCols;
-  const auto part = [&](int i) {
-    return p.parts + (size_t)(2 * (to.z + i) + (i == 0)) * G::slot;
-  };
-  float M = -INFINITY, M2 = -INFINITY, L = 0.f;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = share; i < to.w; i += kSplit) {
-    const float* from = part(i);
-    const float m = from[G::rows * D + r], l = from[G::rows * D + G::rows + r],
-                m2 = from[G::rows * D + 2 * G::rows + r];
-    const float4 y = *reinterpret_cast<const float4*>(from + r * D + col * 4);
-    const float top = fmaxf(M, m), top2 = fmaxf(M2, m2);
-    L = L * weight(M, top) + l * weight(m, top);
-    const float a = weight(M2, top2), e = weight(m2, top2);
-    sum.x = sum.x * a + y.x * e, sum.y = sum.y * a + y.y * e;
-    sum.z = sum.z * a + y.z * e, sum.w = sum.w * a + y.w * e;
-    M = top, M2 = top2;
-  }
-  sums[share][col] = sum;
-  if (col == 0) stats[share][0] = M, stats[share][1] = L, stats[share][2] = M2;
-  __syncthreads();
-  if (share) return;
-  for (int i = 1; i < kSplit; ++i) {
-    const float m = stats[i][0], l = stats[i][1], m2 = stats[i][2];
-    const float4 y = sums[i][col];
-    const float top = fmaxf(M, m), top2 = fmaxf(M2, m2);
-    L = L * weight(M, top) + l * weight(m, top);
-    const float a = weight(M2, top2), e = weight(m2, top2);
-    sum.x = sum.x * a + y.x * e, sum.y = sum.y * a + y.y * e;
-    sum.z = sum.z * a + y.z * e, sum.w = sum.w * a + y.w * e;
-    M = top, M2 = top2;
-  }
-  finish<QT, CT, D>(p, to.x, to.y / p.row_groups, to.y % p.row_groups * G::rows + r, col * 4,
-                    length(p, to.x), sum, M, L, M2);
-}
-
-// ------------------------------------------------------------------- host
-// Pages as [pages][heads][slots][dim], boxes of 16 slots x 128 bytes at most.
-bool page_map(CUtensorMap* map, const void* pages, const pq2_kv_cache& c) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const int e = c.dtype == PQ2_I8 ? 1 : 2;
-  const int row = (int)c.dim * e, box_bytes = row < 128 ? row : 128;
-  // Strides of dimensions with one element are never walked, but must be valid.
-  const auto stride = [&](int64_t n, int64_t s) { return (cuuint64_t)(n > 1 ? s * e : row); };
-  const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads,
-                              (cuuint64_t)c.pages};
-  const cuuint64_t strides[3] = {stride(c.page_size, c.token_stride),
-                                 stride(c.heads, c.head_stride), stride(c.pages, c.page_stride)};
-  const cuuint32_t box[4] = {(cuuint32_t)(box_bytes / e), 16, 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  const CUtensorMapDataType type = c.dtype == PQ2_I8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : c.dtype == PQ2_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return enc(map, type, 4, const_cast<void*>(pages), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool scale_map(CUtensorMap* map, const float* scales, const pq2_kv_cache& c) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)c.page_size * 4, (cuuint64_t)(c.page_size * c.heads) * 4};
-  const cuuint32_t box[3] = {16, 1, 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(scales), dims, strides,
-             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <typename QT, typename CT, int D, int RT>
-int launch(Params& p, int sm_count, cudaStream_t stream) {
-  using G = Geo<CT, D, RT>;
-  auto kern = decode_kernel<QT, CT, D, RT>;
-  static bool configured = false;
-  if (!configured) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return PQ2_ERR_LAUNCH;
-    }
-    configured = true;
-  }
-  CUtensorMap mk{}, mv{}, mks{}, mvs{};
-  if (!page_map(&mk, p.cache.k, p.cache) || !page_map(&mv, p.cache.v, p.cache) ||
-      (G::eight && (!scale_map(&mks, p.cache.k_scales, p.cache) ||
-                    !scale_map(&mvs, p.cache.v_scales, p.cache))))
-    return PQ2_ERR_LAUNCH;
-  p.row_groups = (p.rows + G::rows - 1) / G::rows;
-  p.items = (int)p.cache.heads * p.row_groups;
-  const int ctas = p.cluster ? p.a.batch.B * p.items * kCluster : std::min(sm_count, kMaxCtas);
-  p.places = reinterpret_cast<int4*>(p.a.workspace);
-  p.parts = reinterpret_cast<float*>(p.a.workspace + kMaxCtas * sizeof(int4));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(G::threads);
-  cfg.dynamicSmemBytes = G::smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {kCluster, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = p.cluster ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kern, mk, mv, mks, mvs, p) != cudaSuccess) {
-    cudaGetLastError();
-    return PQ2_ERR_LAUNCH;
-  }
-  if (p.cluster) return PQ2_OK;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(ctas, std::min(p.rows, G::rows));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<QT, CT, D, RT>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return PQ2_ERR_LAUNCH;
-  }
-  return PQ2_OK;
-}
-
-template <typename QT, typename CT, int RT>
-int launch_dim(Params& p, int sm_count, cudaStream_t stream) {
-  if (p.cache.dim == 64) return launch<QT, CT, 64, RT>(p, sm_count, stream);
-  if (p.cache.dim == 128) return launch<QT, CT, 128, RT>(p, sm_count, stream);
-  return launch<QT, CT, 256, RT>(p, sm_count, stream);
-}
-
-template <typename QT, typename CT>
-int launch_rows(Params& p, int sm_count, cudaStream_t stream) {
-  return p.rows <= kRows ? launch_dim<QT, CT, 1>(p, sm_count, stream)
-                         : launch_dim<QT, CT, 2>(p, sm_count, stream);
-}
-
-}  // namespace
-
-namespace {
-
-int tile_rows(int64_t rows) { return rows <= kRows ? kRows : 2 * kRows; }
+// Rows of a CTA, as launch_rows chooses them.
+int group_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 bool in_clusters(int64_t B, int64_t rows, int64_t heads, int64_t positions) {
-  const int n = tile_rows(rows);
+  const int n = group_rows(rows);
   return B * heads * ((rows + n - 1) / n) <= kClusterItems && positions <= kClusterPositions;
 }
 
@@ -1045,22 +20,21 @@ size_t attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_
                                    int64_t dim, int64_t positions) {
   const int64_t rows = T * (q_heads / heads);
   if (in_clusters(B, rows, heads, positions)) return 0;
-  return kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * tile_rows(rows) * (dim + 3) * sizeof(float);
+  return kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * group_rows(rows) * (dim + 3) * sizeof(float);
 }
 
 int launch_attn_decode(const DecodeParams& a, const pq2_kv_cache& c, int sm_count,
                        cudaStream_t stream) {
-  Params p{};
+  AttnDecode p{};
   p.a = a, p.cache = c;
   p.group = a.q_heads / (int)c.heads;
   p.rows = a.T * p.group;
   p.c = a.scale * kLog2e;
   p.cluster = in_clusters(a.batch.B, p.rows, c.heads, a.batch.table_width * c.page_size);
+  if (c.dtype == PQ2_I8) return launch_attn_decode8(p, sm_count, stream);
   if (a.dtype == PQ2_BF16)
-    return c.dtype == PQ2_I8 ? launch_rows<__nv_bfloat16, int8_t>(p, sm_count, stream)
-                             : launch_rows<__nv_bfloat16, __nv_bfloat16>(p, sm_count, stream);
-  return c.dtype == PQ2_I8 ? launch_rows<__half, int8_t>(p, sm_count, stream)
-                           : launch_rows<__half, __half>(p, sm_count, stream);
+    return launch_rows<__nv_bfloat16, __nv_bfloat16>(p, sm_count, stream);
+  return launch_rows<__half, __half>(p, sm_count, stream);
 }
 
 }  // namespace pq2
