@@ -33,8 +33,8 @@ int launch_attn_decode(const DecodeParams& a, const pq2_kv_cache& c, int sm_coun
   p.cluster = in_clusters(a.batch.B, p.rows, c.heads, a.batch.table_width * c.page_size);
   if (c.dtype == PQ2_I8) return launch_attn_decode8(p, sm_count, stream);
   if (a.dtype == PQ2_BF16)
-    return launch_rows<__nv_bfloat16, __nv_bfloat16>(p, sm_count, stream);
-  return launch_rows<__half, __half>(p, sm_count, stream);
+    return launch_dim<__nv_bfloat16, __nv_bfloat16>(p, sm_count, stream);
+  return launch_dim<__half, __half>(p, sm_count, stream);
 }
 
 }  // namespace pq2

@@ -69,11 +69,12 @@ constexpr int kScaleBytes = 128;  // of 16 scales: a copy's target is 128-byte a
 template <typename CT, int D, int RT, int NB>
 struct Geo {
   static constexpr bool eight = sizeof(CT) == 1;
-  static constexpr int warps = eight && D <= 128 ? 12 : 8, slices = warps / RT;
+  static constexpr int warps = eight && D <= 128 && NB <= 2 ? 12 : 8, slices = warps / RT;
   static constexpr int threads = warps * 32;
   // Tokens of a slice: 32 codes share the steps between the MMAs; 16 elements
-  // of 16 bits leave that off the critical path and cut short contexts finer.
-  static constexpr int boxes16 = eight ? 2 : 1, tokens = 16 * boxes16;
+  // of 16 bits leave that off the critical path and cut short contexts finer
+  // (as does a thread of 32 rows, whose registers have no room for more).
+  static constexpr int boxes16 = eight && NB < 4 ? 2 : 1, tokens = 16 * boxes16;
   static constexpr int tile = slices * tokens;      // tokens that a CTA takes at a time
   static constexpr int rowBytes = D * (int)sizeof(CT);
   static constexpr int boxBytes = rowBytes < 128 ? rowBytes : 128;
@@ -458,13 +459,13 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
       }
     }
   };
-  // The next unit's copies; for several row tiles the first one's warp makes
-  // them when all have read what the ring holds there.
+  // The next unit's copies; where RT warps share the slice, the first of them
+  // makes them when all have read what the ring holds there.
   const auto issue = [&]() {
     if (copy.left <= 0) return;
     const uint32_t st = issued % G::depth;
     if (RT > 1 && rt == 0 && issued >= G::depth)
-      ok = ok && mbar_wait(&freed[st], issued / G::depth - 1 & 1);
+      ok = ok && mbar_wait(&freed[st], (issued / G::depth - 1) & 1);
     const int from = (copy.tile - pages_tile) * G::boxes16;
     int page[G::boxes16], slot[G::boxes16];
 #pragma unroll
@@ -502,8 +503,10 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
     ++used;
   };
   seek();
+  // Where warps share a slice, one less: a unit's place is then filled again when
+  // the next one has been read, which the others have mostly done too.
 #pragma unroll 1
-  for (int i = 0; i < G::depth; ++i) issue();
+  for (int i = 0; i < G::depth - (RT > 1); ++i) issue();
 
   // Lane addresses inside 16 tokens of a unit.  An A fragment's matrices are
   // (rows 0-7 and 8-15) x (columns 0-7 and 8-15), the second half of the rows
@@ -1080,18 +1083,19 @@ int launch(Params& p, int sm_count, cudaStream_t stream) {
   return PQ2_OK;
 }
 
-template <typename QT, typename CT, int RT, int NB>
-int launch_dim(Params& p, int sm_count, cudaStream_t stream) {
-  if (p.cache.dim == 64) return launch<QT, CT, 64, RT, NB>(p, sm_count, stream);
-  if (p.cache.dim == 128) return launch<QT, CT, 128, RT, NB>(p, sm_count, stream);
-  return launch<QT, CT, 256, RT, NB>(p, sm_count, stream);
+template <typename QT, typename CT, int D>
+int launch_rows(Params& p, int sm_count, cudaStream_t stream) {
+  if (p.rows <= 8) return launch<QT, CT, D, 1, 1>(p, sm_count, stream);
+  if (p.rows <= 16) return launch<QT, CT, D, 1, 2>(p, sm_count, stream);
+  // 32 rows of 256 columns are more than a thread's registers.
+  return launch<QT, CT, D, D <= 128 ? 1 : 2, D <= 128 ? 4 : 2>(p, sm_count, stream);
 }
 
 template <typename QT, typename CT>
-int launch_rows(Params& p, int sm_count, cudaStream_t stream) {
-  if (p.rows <= 8) return launch_dim<QT, CT, 1, 1>(p, sm_count, stream);
-  if (p.rows <= 16) return launch_dim<QT, CT, 1, 2>(p, sm_count, stream);
-  return launch_dim<QT, CT, 2, 2>(p, sm_count, stream);
+int launch_dim(Params& p, int sm_count, cudaStream_t stream) {
+  if (p.cache.dim == 64) return launch_rows<QT, CT, 64>(p, sm_count, stream);
+  if (p.cache.dim == 128) return launch_rows<QT, CT, 128>(p, sm_count, stream);
+  return launch_rows<QT, CT, 256>(p, sm_count, stream);
 }
 
 }  // namespace
