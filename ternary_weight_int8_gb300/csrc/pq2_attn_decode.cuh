@@ -71,10 +71,9 @@ struct Geo {
   static constexpr bool eight = sizeof(CT) == 1;
   static constexpr int warps = eight && D <= 128 && NB <= 2 ? 12 : 8, slices = warps / RT;
   static constexpr int threads = warps * 32;
-  // Tokens of a slice: 32 codes share the steps between the MMAs; 16 elements
-  // of 16 bits leave that off the critical path and cut short contexts finer
-  // (as does a thread of 32 rows, whose registers have no room for more).
-  static constexpr int boxes16 = eight && NB < 4 ? 2 : 1, tokens = 16 * boxes16;
+  // Tokens of a slice: 32 share the steps between the MMAs where a thread's
+  // registers and the ring have room for them.
+  static constexpr int boxes16 = NB < 4 && (eight || D <= 128) ? 2 : 1, tokens = 16 * boxes16;
   static constexpr int tile = slices * tokens;      // tokens that a CTA takes at a time
   static constexpr int rowBytes = D * (int)sizeof(CT);
   static constexpr int boxBytes = rowBytes < 128 ? rowBytes : 128;
