@@ -786,7 +786,7 @@ int pq2_kv_store(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
   const pq2::KvBatch b{table, cu, lens, table_stride, (int)table_width, (int)B, tokens};
   return pq2::launch_kv_store({const_cast<void*>(k), k_token_stride, k_head_stride},
                               {const_cast<void*>(v), v_token_stride, v_head_stride}, dtype,
-                              *cache, b, static_cast<cudaStream_t>(stream));
+                              *cache, b, sms, static_cast<cudaStream_t>(stream));
 }
 
 int pq2_kv_load(const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
@@ -802,7 +802,7 @@ int pq2_kv_load(const pq2_kv_cache* cache, const int32_t* table, int64_t table_s
   if (int st = device_check(&sms)) return st;
   if (!tokens) return PQ2_OK;
   const pq2::KvBatch b{table, cu, lens, table_stride, (int)table_width, (int)B, tokens};
-  return pq2::launch_kv_load(*cache, b, k, v, dtype, static_cast<cudaStream_t>(stream));
+  return pq2::launch_kv_load(*cache, b, k, v, dtype, sms, static_cast<cudaStream_t>(stream));
 }
 
 namespace {

@@ -133,9 +133,9 @@ struct KvRows {
   int64_t token_stride, head_stride;
 };
 int launch_kv_store(KvRows k, KvRows v, int dtype, const pq2_kv_cache& c, const KvBatch& b,
-                    cudaStream_t stream);
+                    int sm_count, cudaStream_t stream);
 int launch_kv_load(const pq2_kv_cache& c, const KvBatch& b, void* k, void* v, int dtype,
-                   cudaStream_t stream);
+                   int sm_count, cudaStream_t stream);
 
 struct DecodeParams {
   const void* q;
