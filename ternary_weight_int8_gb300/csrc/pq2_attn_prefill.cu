@@ -199,13 +199,29 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;   // per query tile
   uint64_t* s_full = q_full + kTiles;   // per score buffer
-  uint64_t* p_full = s_full + G::slots;
+  uint64_t* p_half = s_full + G::slots; // the first half of the weights, all of them
+  uint64_t* p_full = p_half + G::slots;
   uint64_t* o_full = p_full + G::slots; // per query tile
   uint32_t* tmem_addr_s = reinterpret_cast<uint32_t*>(o_full + kTiles);
   int* sums = reinterpret_cast<int*>(tmem_addr_s + 1);  // per warp, then the CTA's place
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarps = G::threads / 32;
+  // What does not wait for the kernel before.
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < kTiles; ++i) mbar_init(&q_full[i], 1), mbar_init(&o_full[i], 1);
+    for (int i = 0; i < G::slots; ++i)
+      mbar_init(&s_full[i], 1), mbar_init(&p_half[i], 4), mbar_init(&p_full[i], 4);
+    fence_barrier_init();
+  }
+  if (warp == G::copyWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+  }
+  int* place = sums + kWarps;  // sequence, tile, its rows and keys; tiles so far
+  if (tid == 0) place[0] = -1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -217,44 +233,40 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
   const auto row_of = [&](const int32_t* cu, int i, int rows) {
     return min(max(__ldg(cu + i), 0), rows);
   };
-  int seq = -1, tile = 0;
-  {
-    int* place = sums + kWarps;
-    if (tid == 0) place[0] = -1;
-    int behind = 0;  // tiles of the sequences behind those looked at
-    for (int last = p.B; last > 0 && behind <= nth; last -= G::threads) {
-      const int b = last - 1 - tid;
-      int n = 0;
-      if (b >= 0) n = max(row_of(p.cu_q, b + 1, p.q_rows) - row_of(p.cu_q, b, p.q_rows), 0);
-      n = (n + per - 1) / per;
-      int upto = n;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += x;
-      }
-      if (lane == 31) sums[warp] = upto;
-      __syncthreads();
-      int before = behind;
-      for (int w = 0; w < warp; ++w) before += sums[w];
-      upto += before;
-      if (nth < upto && nth >= upto - n) place[0] = b, place[1] = upto - 1 - nth;
-      behind = upto;
-      if (tid == G::threads - 1) place[2] = behind;
-      __syncthreads();
-      behind = place[2];
-      __syncthreads();
+  int behind = 0;  // tiles of the sequences behind those looked at
+  for (int last = p.B; last > 0 && behind <= nth; last -= G::threads) {
+    const int b = last - 1 - tid;
+    int n = 0, q0 = 0, k0 = 0, nk = 0;
+    if (b >= 0) {
+      q0 = row_of(p.cu_q, b, p.q_rows), k0 = row_of(p.cu_k, b, p.k_rows);
+      n = max(row_of(p.cu_q, b + 1, p.q_rows) - q0, 0);
+      nk = max(row_of(p.cu_k, b + 1, p.k_rows) - k0, 0);
     }
+    const int tiles = (n + per - 1) / per;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    seq = place[0], tile = place[1];
+    upto += behind;
+    int all = behind;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int x = sums[w];
+      upto += w < warp ? x : 0, all += x;
+    }
+    if (nth < upto && nth >= upto - tiles) {
+      place[0] = b, place[1] = upto - 1 - nth;
+      place[2] = q0, place[3] = n, place[4] = k0, place[5] = nk;
+    }
+    behind = all;
     __syncthreads();
   }
-  if (seq < 0) return;
-
-  const int q0 = row_of(p.cu_q, seq, p.q_rows);
-  const int nq = row_of(p.cu_q, seq + 1, p.q_rows) - q0;
-  const int k0 = row_of(p.cu_k, seq, p.k_rows);
-  const int nk = max(row_of(p.cu_k, seq + 1, p.k_rows) - k0, 0);
+  if (place[0] < 0) return;
+  const int tile = place[1], q0 = place[2], nq = place[3], k0 = place[4], nk = place[5];
   // The keys that token t sees.
   const auto sees = [&](int t) { return p.causal ? min(max(nk - nq + t + 1, 0), nk) : nk; };
   int first[kTiles], count[kTiles], most_tiles = 0;  // first token, key tiles
@@ -265,12 +277,6 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     most_tiles = max(most_tiles, count[s]);
   }
 
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < kTiles; ++i) mbar_init(&q_full[i], 1), mbar_init(&o_full[i], 1);
-    for (int i = 0; i < G::slots; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
-    fence_barrier_init();
-  }
   if (warp == G::mmaWarp) {
     tmem_alloc(tmem_addr_s, 512);
     tmem_relinquish();
@@ -285,8 +291,6 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
   // tile's K, then the V of the tile before (dim 256: one further behind).
   if (warp == G::copyWarp) {
     if (lane == 0 && most_tiles > 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
       int use = 0;
       const auto pieces = [&](const CUtensorMap* map, int j) {
         for (int i = 0; i < G::pieces; ++i, ++use) {
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     };
     // out += P V of tile s, V's pieces at ring position `use`.
     const auto product = [&](int s, int slot, int use, int j, bool release, bool clean) {
-      ok = ok && mbar_wait(&p_full[slot], (kTiles == 2 ? j : j / 2) & 1);
+      const uint32_t phase = (kTiles == 2 ? j : j / 2) & 1;
+      ok = ok && mbar_wait(&p_half[slot], phase);
 #pragma unroll
       for (int i = 0; i < G::pieces; ++i) {
         const int st = (use + i) % kStages;
@@ -366,9 +371,14 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
         tc_fence_after();
         const uint64_t vd = smem_desc_mn(ring + st * G::piece, BN * 128);
 #pragma unroll
-        for (int x = 0; x < BN / 16; ++x)
+        for (int x = 0; x < BN / 16; ++x) {
+          if (i == 0 && x == BN / 32) {
+            ok = ok && mbar_wait(&p_full[slot], phase);
+            tc_fence_after();
+          }
           mma_f16_ta(on, tmem + G::oCol + s * D + i * G::cols, tmem + slot * BN + x * 8,
                      vd + ((x * 2048) >> 4), idesc_pv, j > 0 || x > 0);
+        }
         if (release) mma_commit(on, &empty[st]);
       }
       mma_commit(on, &o_full[s]);
@@ -465,6 +475,9 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
           tmem_st_wait();
         }
       }
+      // With one tile the last product but one may still be running here; a
+      // phase further and the wait for the last one could not tell them apart.
+      if (kTiles == 1 && j > 0 && j + 1 == tiles) ok = ok && mbar_wait(&o_full[0], (j - 1) & 1);
       const float mc = m == -INFINITY ? 0.f : m * p.c;
 #pragma unroll
       for (int i = 0; i < BN; i += 32) {
@@ -480,11 +493,15 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
           w[e / 2] = pack<T>(a, b), w[e / 2 + 1] = pack<T>(c, d);
         }
         tmem_st16(s_tmem + i / 2, w);
+        if (i == BN / 2 - 32) {
+          // The products with the first half of the keys can begin.
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          warp_arrive(&p_half[slot]);
+        }
       }
       tmem_st_wait();
-      // With one tile the last product but one may still be running here; a
-      // phase further and the wait for the last one could not tell them apart.
-      if (kTiles == 1 && j > 0 && j + 1 == tiles) ok = ok && mbar_wait(&o_full[0], (j - 1) & 1);
       tc_fence_before();
       __syncwarp();
       warp_arrive(&p_full[slot]);
@@ -495,14 +512,22 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
       tc_fence_after();
     }
     const int h = head * p.group + r % p.group;
-    const int64_t row = ((int64_t)q0 + t) * p.q_heads + h;
-    T* out = static_cast<T*>(p.out) + row * D;
+    const int64_t row = live ? ((int64_t)q0 + t) * p.q_heads + h : -1;
     const float factor = most > 0 ? 1.f / l : 0.f;
     const float mc = m == -INFINITY ? 0.f : m * p.c;
+    // Through the query tile's place in shared memory, which the scores have
+    // read for the last time: a thread's row there, then whole rows by all lanes
+    // (a thread's own row straight to global memory took 32 lines a store, 5000
+    // clocks at dim 128).
+    uint8_t* rows = smem + s * G::qBytes + (warp & 3) * 32 * 128;
+    const auto staged = [&](int r, int d) {
+      return reinterpret_cast<uint4*>(rows + d / 64 * (BM * 128) + r * 128 +
+                                      ((d / 8 % 8 ^ (r & 7)) << 4));
+    };
+    uint32_t bad = 0;  // groups of 32 columns that are not finite
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       float o[32];
-      __syncwarp();
       if (tiles) {
         tmem_ld32(o_tmem + d, o);
         tmem_ld_wait();
@@ -513,15 +538,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
         if (most <= 0) o[i] = 0.f;
         zero = fmaf(o[i], 0.f, zero);
       }
-      if (!live) continue;
-      if (zero != 0.f && factor - factor == 0.f) {
-        const T* q = static_cast<const T*>(p.q) + ((int64_t)q0 + t) * p.q_token + h * p.q_head;
-        const T* k = static_cast<const T*>(p.k) + (int64_t)k0 * p.k_token + head * p.k_head;
-        const T* v = static_cast<const T*>(p.v) + (int64_t)k0 * p.v_token + head * p.v_head + d;
-        plain_columns<T, D>(q, k, p.k_token, v, p.v_token, most, p.negative ? -p.c : p.c, mc,
-                            factor, out + d);
-        continue;
-      }
+      if (zero != 0.f) bad |= 1u << d / 32;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         uint4 w;
@@ -529,11 +546,27 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
         w.y = pack<T>(o[i + 2] * factor, o[i + 3] * factor);
         w.z = pack<T>(o[i + 4] * factor, o[i + 5] * factor);
         w.w = pack<T>(o[i + 6] * factor, o[i + 7] * factor);
-        *reinterpret_cast<uint4*>(out + d + i) = w;
+        *staged(lane, d + i) = w;
       }
     }
-    if (live && p.lse)
-      p.lse[row] = most > 0 ? mc * kLn2 + logf(l) : -INFINITY;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const int piece = i * 32 + lane, of = piece / (D / 8), d = piece % (D / 8) * 8;
+      const int64_t to = __shfl_sync(~0u, row, of);
+      if (to >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to * D + d) = *staged(of, d);
+    }
+    __syncwarp();
+    if (live && p.lse) p.lse[row] = most > 0 ? mc * kLn2 + logf(l) : -INFINITY;
+    if (live && bad && factor - factor == 0.f) {
+      const T* q = static_cast<const T*>(p.q) + ((int64_t)q0 + t) * p.q_token + h * p.q_head;
+      const T* k = static_cast<const T*>(p.k) + (int64_t)k0 * p.k_token + head * p.k_head;
+      const T* v = static_cast<const T*>(p.v) + (int64_t)k0 * p.v_token + head * p.v_head;
+      for (int d = 0; d < D; d += 32)
+        if (bad >> d / 32 & 1)
+          plain_columns<T, D>(q, k, p.k_token, v + d, p.v_token, most, p.negative ? -p.c : p.c, mc,
+                              factor, static_cast<T*>(p.out) + row * D + d);
+    }
   }
   if (!ok) report(p.status, PQ2_ERR_TIMEOUT);
   tc_fence_before();
