@@ -23,6 +23,10 @@
 // tile's two products (dim 256: the next key tile's scores, in a second
 // buffer, and the last one's P V), so neither waits for the other for long.
 //
+// Few query tiles before many keys leave SMs without work: then `splits` CTAs
+// take a part of a tile's keys each and write out, m and l in 32 bits, and a
+// second kernel joins them.
+//
 // Bound: the MMAs, 4 * 128 * 128 * dim operations a tile pair of 128 x 128.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,6 +74,9 @@ struct Params {
   float c;        // |scale| / ln 2
   int negative;   // scale < 0
   int causal;
+  int splits;     // of a tile's keys; with more than one:
+  float* parts;   // [splits][q_rows][q_heads][dim], sums of weights times values
+  float2* stats;  // [splits][q_rows][q_heads], maximum (powers of two) and sum of weights
 };
 
 // Shared-memory matrix descriptor of a 128-byte swizzled operand whose M or N
@@ -266,9 +273,23 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     __syncthreads();
   }
   if (place[0] < 0) return;
-  const int tile = place[1], q0 = place[2], nq = place[3], k0 = place[4], nk = place[5];
-  // The keys that token t sees.
-  const auto sees = [&](int t) { return p.causal ? min(max(nk - nq + t + 1, 0), nk) : nk; };
+  const int tile = place[1], q0 = place[2], nq = place[3], k0_all = place[4],
+            nk_all = place[5];
+  // This CTA's part of the keys begins at the tile pair's key tile `from`; keys
+  // are counted from there.
+  int low = 0, high = nk_all;
+  if (p.splits > 1) {
+    const int last = min((tile + 1) * kTiles * p.tokens, nq) - 1;
+    const int all = ((p.causal ? min(max(nk_all - nq + last + 1, 0), nk_all) : nk_all) + BN - 1) / BN;
+    low = (int)((int64_t)blockIdx.y * all / p.splits) * BN;
+    high = min((int)((int64_t)(blockIdx.y + 1) * all / p.splits) * BN, nk_all);
+  }
+  const int k0 = k0_all + low, nk = nk_all - low;
+  // The keys of its part that token t sees.
+  const auto sees = [&](int t) {
+    const int n = p.causal ? min(nk_all - nq + t + 1, nk_all) : nk_all;
+    return max(min(n, high) - low, 0);
+  };
   int first[kTiles], count[kTiles], most_tiles = 0;  // first token, key tiles
 #pragma unroll
   for (int s = 0; s < kTiles; ++s) {
@@ -524,6 +545,40 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
       return reinterpret_cast<uint4*>(rows + d / 64 * (BM * 128) + r * 128 +
                                       ((d / 8 % 8 ^ (r & 7)) << 4));
     };
+    if (p.splits > 1) {
+      // Two rounds of half the columns, in 32 bits.
+      const int64_t part = (int64_t)blockIdx.y * p.q_rows * p.q_heads;
+      if (live) p.stats[part + row] = make_float2(m == -INFINITY ? m : mc, l);
+#pragma unroll 1
+      for (int round = 0; round < 2; ++round) {
+#pragma unroll 1
+        for (int d = 0; d < D / 2; d += 32) {
+          float o[32];
+          if (tiles) {
+            tmem_ld32(o_tmem + round * (D / 2) + d, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (tiles)
+              w = make_uint4(__float_as_uint(o[i]), __float_as_uint(o[i + 1]),
+                             __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3]));
+            *staged(lane, (d + i) * 2) = w;
+          }
+        }
+        __syncwarp();
+#pragma unroll 2
+        for (int i = 0; i < D / 8; ++i) {
+          const int piece = i * 32 + lane, of = piece / (D / 8), d = piece % (D / 8) * 4;
+          const int64_t to = __shfl_sync(~0u, row, of);
+          if (to >= 0)
+            *reinterpret_cast<uint4*>(p.parts + (part + to) * D + round * (D / 2) + d) =
+                *staged(of, d * 2);
+        }
+        __syncwarp();
+      }
+    } else {
     uint32_t bad = 0;  // groups of 32 columns that are not finite
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
@@ -567,6 +622,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
           plain_columns<T, D>(q, k, p.k_token, v + d, p.v_token, most, p.negative ? -p.c : p.c, mc,
                               factor, static_cast<T*>(p.out) + row * D + d);
     }
+    }
   }
   if (!ok) report(p.status, PQ2_ERR_TIMEOUT);
   tc_fence_before();
@@ -574,6 +630,75 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
   if (warp == G::mmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a row: a warp for each, D / 32 neighbouring columns a lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const Params p) {
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, i = (int)(row / p.q_heads), h = (int)(row % p.q_heads);
+  const auto bound = [&](const int32_t* cu, int b, int rows) {
+    return min(max(__ldg(cu + b), 0), rows);
+  };
+  if (i >= p.q_rows || i < bound(p.cu_q, 0, p.q_rows) || i >= bound(p.cu_q, p.B, p.q_rows)) return;
+  const int64_t step = (int64_t)p.q_rows * p.q_heads;
+  const float2 ml = lane < p.splits ? p.stats[lane * step + row] : make_float2(-INFINITY, 0.f);
+  float m = ml.x, l;
+#pragma unroll
+  for (int o = 16; o; o /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  const float weight = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+  l = ml.y * weight;
+  if (ml.y == 0.f) l = 0.f;
+#pragma unroll
+  for (int o = 16; o; o /= 2) l += __shfl_xor_sync(~0u, l, o);
+  float sum[E] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float w = __shfl_sync(~0u, weight, s);
+    if (w == 0.f) continue;
+    const float* from = p.parts + (s * step + row) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(from + e);
+      sum[e] = fmaf(y.x, w, sum[e]), sum[e + 1] = fmaf(y.y, w, sum[e + 1]);
+    }
+  }
+  float zero = l - l;  // NaN if something is not finite
+#pragma unroll
+  for (int e = 0; e < E; ++e) zero = fmaf(sum[e], 0.f, zero);
+  T* out = static_cast<T*>(p.out) + row * D;
+  // Rows with sums that are not finite, or that see nothing: which keys do they
+  // see?
+  const bool odd = __any_sync(~0u, zero != 0.f) || l == 0.f;
+  int most = 1, k0 = 0;
+  if (odd) {
+    int lo = 0, hi = p.B + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu_q + mid) <= i) lo = mid + 1; else hi = mid;
+    }
+    const int b = max(min(lo - 1, p.B - 1), 0), q0 = bound(p.cu_q, b, p.q_rows);
+    const int nq = bound(p.cu_q, b + 1, p.q_rows) - q0;
+    k0 = bound(p.cu_k, b, p.k_rows);
+    const int nk = max(bound(p.cu_k, b + 1, p.k_rows) - k0, 0);
+    most = p.causal ? min(max(nk - nq + (i - q0) + 1, 0), nk) : nk;
+  }
+  const float factor = most > 0 ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(out + lane * E + e) =
+        most > 0 ? pack<T>(sum[e] * factor, sum[e + 1] * factor) : 0u;
+  if (lane == 0 && p.lse) p.lse[row] = most > 0 ? m * kLn2 + logf(l) : -INFINITY;
+  __syncwarp();
+  if (odd && most > 0 && factor - factor == 0.f && lane < E) {
+    const int kh = h / p.group, d = lane * 32;
+    plain_columns<T, D>(static_cast<const T*>(p.q) + i * p.q_token + h * p.q_head,
+                        static_cast<const T*>(p.k) + k0 * p.k_token + kh * p.k_head, p.k_token,
+                        static_cast<const T*>(p.v) + k0 * p.v_token + kh * p.v_head + d, p.v_token,
+                        most, p.negative ? -p.c : p.c, m, factor, out + d);
   }
 }
 
@@ -596,6 +721,23 @@ bool row_map(CUtensorMap* map, const KvRows& r, int64_t rows, int heads, int dim
              3, r.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// As many tile pairs (dim 256: tiles) as the sequences can have at most.
+int64_t tile_pairs(int64_t B, int64_t q_rows, int64_t group, int64_t dim) {
+  const int64_t per = (dim <= 128 ? 2 : 1) * (BM / group);
+  return std::min(q_rows, (q_rows + per - 1) / per + B - 1);
+}
+// Parts of a tile's keys: as many as fill one wave of 152 SMs, of at least 8
+// key tiles on average, 16 at most.  64 rows of 40 heads after 16000 keys, 9
+// parts: 152 -> 32 us; but 300 tile pairs in two parts: 355 -> 392 us (dim 256,
+// 16896 keys), 328 in two: 44 -> 93 us (dim 128, 2048 keys), for what the parts
+// write and read.
+int key_splits(int64_t B, int64_t q_rows, int64_t k_rows, int64_t q_heads, int64_t heads,
+               int64_t dim) {
+  const int64_t ctas = tile_pairs(B, q_rows, q_heads / heads, dim) * heads;
+  return (int)std::max<int64_t>(
+      1, std::min<int64_t>({16, 152 / ctas, k_rows / (B * 8 * BN)}));
 }
 
 template <typename T, int D>
@@ -636,12 +778,14 @@ int launch(const PrefillParams& a, cudaStream_t stream) {
       !row_map(&mk, k, rows, heads, D, a.dtype, 1, BN) ||
       !row_map(&mv, v, rows, heads, D, a.dtype, 1, BN))
     return PQ2_ERR_LAUNCH;
-  // As many tiles as the sequences can have at most.
-  const int per = G::tiles * p.tokens;
-  const int64_t tiles = std::min<int64_t>(a.q_rows, (a.q_rows + per - 1) / per + a.B - 1);
-  if (tiles * a.heads > 0x7fffffff) return PQ2_ERR_SHAPE;
+  const int64_t tiles = tile_pairs(a.B, a.q_rows, p.group, D);
+  if (tiles * a.heads > 0x7fffffff || (a.q_rows * a.q_heads + 7) / 8 > 0x7fffffff)
+    return PQ2_ERR_SHAPE;
+  p.splits = key_splits(a.B, a.q_rows, a.k_rows, a.q_heads, a.heads, D);
+  p.parts = reinterpret_cast<float*>(a.workspace);
+  p.stats = reinterpret_cast<float2*>(p.parts + (size_t)p.splits * a.q_rows * a.q_heads * D);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * a.heads));
+  cfg.gridDim = dim3((unsigned)(tiles * a.heads), p.splits);
   cfg.blockDim = dim3(G::threads);
   cfg.dynamicSmemBytes = G::smem;
   cfg.stream = stream;
@@ -651,6 +795,14 @@ int launch(const PrefillParams& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PQ2_ERR_LAUNCH;
+  }
+  if (p.splits == 1) return PQ2_OK;
+  cfg.gridDim = dim3((unsigned)((a.q_rows * a.q_heads + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&cfg, prefill_join_kernel<T, D>, p) != cudaSuccess) {
     cudaGetLastError();
     return PQ2_ERR_LAUNCH;
   }
@@ -666,8 +818,10 @@ int launch_dim(const PrefillParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t attn_prefill_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) {
-  return 0;
+size_t attn_prefill_workspace_bytes(int64_t B, int64_t q_rows, int64_t k_rows, int64_t q_heads,
+                                    int64_t heads, int64_t dim) {
+  const int splits = key_splits(B, q_rows, k_rows, q_heads, heads, dim);
+  return splits == 1 ? 0 : (size_t)splits * q_rows * q_heads * (dim + 2) * sizeof(float);
 }
 
 int launch_attn_prefill(const PrefillParams& p, int sm_count, cudaStream_t stream) {

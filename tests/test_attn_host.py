@@ -120,6 +120,12 @@ def test_prefill_refusals(L):
             (8, 4, ALIGN), (0, A + 8, ALIGN), (3, A + 2, ALIGN), (20, A + 8, ALIGN),
             (21, A + 1, ALIGN), (15, A + 2, ALIGN))
     f = L.pq2_attn_prefill_workspace_bytes
+    assert f(1, 8192, 8192, 40, 8, 128) == 0 and f(1, 64, 16000, 40, 8, 128) > 0
+    parts = list(ok)
+    parts[10], parts[11], parts[22] = 64, 16000, None
+    assert L.pq2_attn_prefill(*parts) == NULL
+    parts[22], parts[23] = A, 64
+    assert L.pq2_attn_prefill(*parts) == SHAPE
     for bad in ((0, 1, 1, 4, 2, 128), (1, 0, 1, 4, 2, 128), (1, 1, -1, 4, 2, 128),
                 (1, 1, 1, 3, 2, 128), (1, 1, 1, 4, 2, 96)):
         assert f(*bad) == 0

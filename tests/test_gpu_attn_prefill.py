@@ -102,6 +102,54 @@ def test_long(D):
     check(q, k, v, nq, nq, heads=[0, 3])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,H,G", [
+    ([1], [20000], 1, 1), ([70], [9001], 2, 5), ([40, 0, 300], [6000, 50, 12000], 1, 6),
+    ([3, 200], [0, 17000], 2, 3), ([700], [20000], 1, 2), ([300, 5], [70, 5000], 1, 1)])
+def test_few_rows_before_many_keys(dtype, D, causal, nq, nk, H, G):
+    """The keys of a tile in several parts, joined: rows that see none of a part's
+    keys, or none at all, sequences with fewer key tiles than parts."""
+    B, rows, keys = len(nq), sum(nq), sum(nk)
+    nbytes = pq2.lib().pq2_attn_prefill_workspace_bytes(B, rows, keys, H * G, H, D)
+    parts = nbytes // (rows * H * G * (D + 2) * 4)
+    assert parts > 1 and parts * rows * H * G * (D + 2) * 4 == nbytes
+    q, k, v = inputs(nq, nk, H, G, D, dtype, seed=sum(nk) + D, spare=3)
+    check(q, k, v, nq, nk, causal=causal, heads=[0, H * G - 1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_seen_in_parts(D, bad):
+    """A later token's value that is not finite stays out of the rows before it in
+    the join too, and is in the rows that see it."""
+    nq, nk = [60], [9000]
+    q, k, v = inputs(nq, nk, 1, 2, D, BF16, seed=5, spare=64)
+    v[8970, 0, 5:9], v[9000:], k[9000:] = bad, bad, bad
+    out = pq2.pq2_attn_prefill(q, k, v, sums(nq), sums(nk))
+    most = 8970 - (9000 - 60)  # rows before it
+    ref = out[:most].clone()
+    verify(ref, None, q[:most], k, v, [most], [8970])
+    assert not bool(out[most:60, :, 5:9].isfinite().any())
+    assert bool(out[most:60, :, 9:].isfinite().all())
+    k[10] = float("nan")
+    assert bool(pq2.pq2_attn_prefill(q, k, v, sums(nq), sums(nk))[:60].isnan().all())
+
+
+def test_a_workspace_of_the_callers():
+    nq, nk = [50, 9], [9000, 5000]
+    q, k, v = inputs(nq, nk, 2, 4, 128, F16, seed=2)
+    want = check(q, k, v, nq, nk)
+    nbytes = pq2.lib().pq2_attn_prefill_workspace_bytes(2, 59, 14000, 8, 2, 128)
+    back = torch.full((nbytes + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    got = pq2.pq2_attn_prefill(q, k, v, sums(nq), sums(nk), workspace=back[256:256 + nbytes])
+    assert torch.equal(got, want)
+    assert bool((back[:256] == 0x5A).all()) and bool((back[256 + nbytes:] == 0x5A).all())
+    with pytest.raises(pq2.Pq2Error):
+        pq2.pq2_attn_prefill(q, k, v, sums(nq), sums(nk), workspace=back[256:256 + nbytes - 16])
+
+
 @pytest.mark.parametrize("B", [1000, 2500])
 def test_many_sequences(B):
     nq = [(7 * b) % 4 for b in range(B)]
