@@ -232,49 +232,71 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // Which sequence and which of its query tiles: the CTAs count them from the
-  // last one back, so that of one long prompt the tiles with the most keys come
-  // first.  A sequence of n rows has ceil(n / (kTiles * tokens)).
+  // Which sequence and which of its query tiles.  A sequence of n rows has
+  // ceil(n / (kTiles * tokens)); the CTAs count them from a sequence's last one
+  // back, so that the tiles with the most keys come first, and up to 32 sequences
+  // by their keys: the longest CTAs first, the short ones fill the gaps.
   const int per = kTiles * p.tokens;
   const int head = blockIdx.x % p.heads, nth = blockIdx.x / p.heads;
   const auto row_of = [&](const int32_t* cu, int i, int rows) {
     return min(max(__ldg(cu + i), 0), rows);
   };
-  int behind = 0;  // tiles of the sequences behind those looked at
-  for (int last = p.B; last > 0 && behind <= nth; last -= G::threads) {
-    const int b = last - 1 - tid;
-    int n = 0, q0 = 0, k0 = 0, nk = 0;
-    if (b >= 0) {
-      q0 = row_of(p.cu_q, b, p.q_rows), k0 = row_of(p.cu_k, b, p.k_rows);
-      n = max(row_of(p.cu_q, b + 1, p.q_rows) - q0, 0);
-      nk = max(row_of(p.cu_k, b + 1, p.k_rows) - k0, 0);
+  const auto sequence = [&](int b, int (&of)[4]) {  // first row, rows, first key, keys
+    of[0] = row_of(p.cu_q, b, p.q_rows), of[2] = row_of(p.cu_k, b, p.k_rows);
+    of[1] = max(row_of(p.cu_q, b + 1, p.q_rows) - of[0], 0);
+    of[3] = max(row_of(p.cu_k, b + 1, p.k_rows) - of[2], 0);
+  };
+  int of[4] = {}, tile;
+  if (p.B <= 32) {
+    if (lane < p.B) sequence(lane, of);
+    const int tiles = (of[1] + per - 1) / per;
+    int before = 0;
+    for (int b = 0; b < p.B; ++b) {
+      const int keys = __shfl_sync(~0u, of[3], b), n = __shfl_sync(~0u, tiles, b);
+      if (keys > of[3] || (keys == of[3] && b > lane)) before += n;
     }
-    const int tiles = (n + per - 1) / per;
-    int upto = tiles;
+    const uint32_t hit = __ballot_sync(~0u, nth >= before && nth < before + tiles);
+    if (!hit) return;
+    const int by = __ffs(hit) - 1;
+    tile = __shfl_sync(~0u, before + tiles, by) - 1 - nth;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int x = __shfl_up_sync(~0u, upto, o);
-      if (lane >= o) upto += x;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    upto += behind;
-    int all = behind;
+    for (int i = 0; i < 4; ++i) of[i] = __shfl_sync(~0u, of[i], by);
+  } else {
+    int behind = 0;  // tiles of the sequences behind those looked at
+    for (int last = p.B; last > 0 && behind <= nth; last -= G::threads) {
+      const int b = last - 1 - tid;
+      int mine[4] = {};
+      if (b >= 0) sequence(b, mine);
+      const int tiles = (mine[1] + per - 1) / per;
+      int upto = tiles;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int x = sums[w];
-      upto += w < warp ? x : 0, all += x;
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      upto += behind;
+      int all = behind;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int x = sums[w];
+        upto += w < warp ? x : 0, all += x;
+      }
+      if (nth < upto && nth >= upto - tiles) {
+        place[0] = b, place[1] = upto - 1 - nth;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) place[2 + i] = mine[i];
+      }
+      behind = all;
+      __syncthreads();
     }
-    if (nth < upto && nth >= upto - tiles) {
-      place[0] = b, place[1] = upto - 1 - nth;
-      place[2] = q0, place[3] = n, place[4] = k0, place[5] = nk;
-    }
-    behind = all;
-    __syncthreads();
+    if (place[0] < 0) return;
+    tile = place[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) of[i] = place[2 + i];
   }
-  if (place[0] < 0) return;
-  const int tile = place[1], q0 = place[2], nq = place[3], k0_all = place[4],
-            nk_all = place[5];
+  const int q0 = of[0], nq = of[1], k0_all = of[2], nk_all = of[3];
   // This CTA's part of the keys begins at the tile pair's key tile `from`; keys
   // are counted from there.
   int low = 0, high = nk_all;
@@ -317,6 +339,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
         for (int i = 0; i < G::pieces; ++i, ++use) {
           const int st = use % kStages;
           if (use >= kStages) ok = ok && mbar_wait(&empty[st], (use / kStages - 1) & 1);
+          if (!ok) return;  // no more copies once a wait has given up
           mbar_arrive_expect_tx(&full[st], G::piece);
           uint8_t* to = smem + G::offRing + st * G::piece;
           for (int x = 0; x < G::cols / 64; ++x)
@@ -744,15 +767,8 @@ template <typename T, int D>
 int launch(const PrefillParams& a, cudaStream_t stream) {
   using G = Geo<D>;
   auto kern = prefill_kernel<T, D>;
-  static bool configured = false;
-  if (!configured) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem) !=
-        cudaSuccess) {
-      cudaGetLastError();
-      return PQ2_ERR_LAUNCH;
-    }
-    configured = true;
-  }
+  static std::atomic<uint64_t> allowed{0};
+  if (!allow_shared(kern, G::smem, allowed)) return PQ2_ERR_LAUNCH;
   Params p{};
   p.cu_q = a.cu_q, p.cu_k = a.cu_k;
   p.q = a.q.p, p.k = a.k.p, p.v = a.v.p;

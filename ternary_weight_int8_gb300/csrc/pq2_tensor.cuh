@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -138,6 +139,22 @@ inline EncodeTiledFn encode_fn() {
       cudaGetLastError();
   });
   return fn;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device, once
+// for each (`done`: a bit per device).
+template <typename K>
+bool allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return false;
+  if (done.load(std::memory_order_acquire) >> device & 1) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or((uint64_t)1 << device, std::memory_order_release);
+  return true;
 }
 
 }  // namespace pq2

@@ -764,29 +764,22 @@ def _on_one_device(first, *others):
         raise ValueError("the tensors' device must be the current device")
 
 
-def _rows_of_heads(t, what, heads=None, dim=None):
-    shape = t.shape
-    if len(shape) != 3 or t.stride(2) != 1 or heads is not None and shape[1] != heads or \
-            dim is not None and shape[2] != dim:
-        raise ValueError(f"{what} must be [rows][heads][dim] with unit stride in dim")
-
-
 def pq2_kv_store(k, v, cache: KVCache, table, lens, cu=None, stream=None):
     """Writes the newest tokens' keys and values k, v [tokens][heads][dim] into
     the cache: sequence b's rows cu[b]..cu[b+1] (cu None: the rows split evenly)
     are its last positions before lens[b]; page table[b][p // page_size] holds
     position p."""
     c, heads, dim = _c_cache(cache)
-    _rows_of_heads(k, "k", heads, dim)
-    _rows_of_heads(v, "v", heads, dim)
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or v.shape != shape or \
+            v.dtype != k.dtype or ks[2] != 1 or vs[2] != 1:
+        raise ValueError("k and v must be [tokens][heads][dim] of one type, with the cache's heads "
+                         "and dim and unit stride in dim")
     dtype = _dtype_of(k)
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must have one shape and type")
     B, stride, width = _check_table(table, lens, cu)
     _on_one_device(k, v, *cache, table, lens, cu)
-    ks, vs = _strides(k), _strides(v)
     _check("pq2_kv_store", lib().pq2_kv_store(
-        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dtype, k.shape[0], c,
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dtype, shape[0], c,
         table.data_ptr(), stride, width, _ptr(cu), lens.data_ptr(), B, _stream(stream)))
 
 
@@ -814,6 +807,9 @@ def pq2_kv_load(cache: KVCache, table, lens, cu=None, tokens=None, out=None,
     return k, v
 
 
+_attn_bytes = {}
+
+
 def _attn_outputs(q, out, lse):
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"Expected a bfloat16 or float16 tensor, not {q.dtype}")
@@ -835,9 +831,11 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
     q.shape[:-1] for the rows' log-sum-exp."""
     L = lib()
     c, kv_heads, dim = _c_cache(cache)
-    shape, st = q.shape, _strides(q)
-    if len(shape) not in (3, 4) or q.stride(-1) != 1 or shape[-1] != dim:
+    shape, st = q.shape, q.stride()
+    if len(shape) not in (3, 4) or st[-1] != 1 or shape[-1] != dim:
         raise ValueError("q must be [B][heads][dim] or [B][T][heads][dim] with unit stride in dim")
+    if 1 in shape:
+        st = _strides(q)
     B, stride, width = _check_table(table, lens)
     if shape[0] != B:
         raise ValueError("q must have a row per row of the table")
@@ -846,8 +844,10 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
     if cache.k.dtype not in (q.dtype, torch.int8):
         raise ValueError("the cache must have q's type, or int8")
     if workspace is None:
-        nbytes = L.pq2_attn_decode_workspace_bytes(B, T, shape[-2], kv_heads, dim,
-                                                   width * cache.k.shape[2])
+        key = (B, T, shape[-2], kv_heads, dim, width * cache.k.shape[2])
+        nbytes = _attn_bytes.get(key)
+        if nbytes is None:
+            nbytes = _attn_bytes[key] = L.pq2_attn_decode_workspace_bytes(*key)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     elif not workspace.is_contiguous():
@@ -868,24 +868,29 @@ def pq2_attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal: bool = True, 
     [rows][heads][dim] attend rows cu_k[b]..cu_k[b+1] (None: the same) of k and
     v [rows][key heads][dim]; causal counts both from their ends.  scale and lse
     as in pq2_attn_decode."""
-    _rows_of_heads(q, "q")
-    _rows_of_heads(k, "k", None, q.shape[2])
-    _rows_of_heads(v, "v", k.shape[1], q.shape[2])
-    if k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("k and v must have one shape, and q's type")
+    q_shape, k_shape, qs, ks, vs = q.shape, k.shape, q.stride(), k.stride(), v.stride()
+    if len(q_shape) != 3 or len(k_shape) != 3 or q_shape[2] != k_shape[2] or \
+            v.shape != k_shape or qs[2] != 1 or ks[2] != 1 or vs[2] != 1:
+        raise ValueError("q, k and v must be [rows][heads][dim] with unit stride in dim, k and v of "
+                         "one shape and q's dim")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v must have q's type")
     cu_k = cu_q if cu_k is None else cu_k
     _check_ints(cu_q, "cu_q")
     _check_ints(cu_k, "cu_k", cu_q.shape[0])
     out = _attn_outputs(q, out, lse)
-    rows, heads, dim = q.shape
-    keys, kv_heads, B = k.shape[0], k.shape[1], cu_q.shape[0] - 1
-    nbytes = lib().pq2_attn_prefill_workspace_bytes(B, rows, keys, heads, kv_heads, dim)
+    rows, heads, dim = q_shape
+    keys, kv_heads, B = k_shape[0], k_shape[1], cu_q.shape[0] - 1
+    if 1 in q_shape or 1 in k_shape:
+        qs, ks, vs = _strides(q), _strides(k), _strides(v)
+    nbytes = 0
+    if workspace is None:
+        nbytes = lib().pq2_attn_prefill_workspace_bytes(B, rows, keys, heads, kv_heads, dim)
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _on_one_device(q, k, v, cu_q, cu_k, out, lse, workspace, status)
-    qs, ks, vs = _strides(q), _strides(k), _strides(v)
     _check("pq2_attn_prefill", lib().pq2_attn_prefill(
         _ptr(q), qs[0], qs[1], _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1], _DT[q.dtype], rows,
         keys, heads, kv_heads, dim, _ptr(cu_q), _ptr(cu_k), B,
