@@ -689,8 +689,8 @@ typedef struct pq2_kv_cache {
  *            d) at row * token_stride + head * head_stride + d (strides in
  *            elements, one pair for each).  Any alignment of whole elements;
  *            16-byte aligned pointers and strides are faster.
- *   tokens   rows of k and v, 0 .. 1<<24; rows outside every sequence are
- *            not read.
+ *   tokens   rows of k and v, 0 .. 1<<24 (0: nothing is done, k and v may be
+ *            NULL); rows outside every sequence are not read.
  *   cache    (host) its description; pages, tables and scales are device
  *            memory.
  *   table    (device) int32 [B][table_width], rows table_stride apart.
@@ -733,7 +733,8 @@ int pq2_kv_load(const pq2_kv_cache *cache, const int32_t *table,
  *   cache    of q's dtype, or PQ2_I8.
  *   q_heads  a multiple of cache->heads, at most 256 times it; T 1 .. 64;
  *            B 1 .. 1<<16.
- *   scale    finite.
+ *   scale    -1e6 .. 1e6.
+ *   lens     (device) int32 [B]; below 0 as 0, above 1<<30 as that.
  *   out      (device) dtype [B][T][q_heads][dim], 16-byte aligned.
  *   lse      (device, may be NULL) fp32 [B][T][q_heads].
  *   workspace (device) pq2_attn_decode_workspace_bytes (positions =

@@ -771,7 +771,7 @@ int pq2_kv_store(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
                  const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
                  int64_t table_width, const int32_t* cu, const int32_t* lens, int64_t B,
                  void* stream) {
-  if (!k || !v) return PQ2_ERR_NULL;
+  if (tokens && (!k || !v)) return PQ2_ERR_NULL;
   if (!valid_dtype(dtype)) return PQ2_ERR_DTYPE;
   if (int st = check_cache(cache)) return st;
   if (int st = check_batch(table, table_stride, table_width, cu, lens, B)) return st;
@@ -792,7 +792,7 @@ int pq2_kv_store(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
 int pq2_kv_load(const pq2_kv_cache* cache, const int32_t* table, int64_t table_stride,
                 int64_t table_width, const int32_t* cu, const int32_t* lens, int64_t B, void* k,
                 void* v, int dtype, int64_t tokens, void* stream) {
-  if (!k || !v) return PQ2_ERR_NULL;
+  if (tokens && (!k || !v)) return PQ2_ERR_NULL;
   if (!valid_dtype(dtype)) return PQ2_ERR_DTYPE;
   if (int st = check_cache(cache)) return st;
   if (int st = check_batch(table, table_stride, table_width, cu, lens, B)) return st;
@@ -813,7 +813,8 @@ bool valid_decode(int64_t B, int64_t T, int64_t q_heads, int64_t heads, int64_t 
          (dim == 64 || dim == 128 || dim == 256) && B * T * q_heads <= ((int64_t)1 << 31) - 1;
 }
 
-bool is_finite(float x) { return x - x == 0.f; }
+// 1 / sqrt(dim) and its like, of either sign; NaN is none.
+bool valid_scale(float x) { return x >= -1e6f && x <= 1e6f; }
 
 }  // namespace
 
@@ -833,7 +834,7 @@ int pq2_attn_decode(const void* q, int dtype, int64_t batch_stride, int64_t toke
   if (int st = check_cache(cache)) return st;
   if (cache->dtype != dtype && cache->dtype != PQ2_I8) return PQ2_ERR_DTYPE;
   if (int st = check_batch(table, table_stride, table_width, nullptr, lens, B)) return st;
-  if (!valid_decode(B, T, q_heads, cache->heads, cache->dim) || !is_finite(scale))
+  if (!valid_decode(B, T, q_heads, cache->heads, cache->dim) || !valid_scale(scale))
     return PQ2_ERR_SHAPE;
   for (int64_t s : {batch_stride, token_stride, head_stride}) {
     if (!valid_stride(s, 2)) return PQ2_ERR_SHAPE;
@@ -885,7 +886,7 @@ int pq2_attn_prefill(const void* q, int64_t q_token_stride, int64_t q_head_strid
                      int32_t* dev_status, void* stream) {
   if (!q || (k_rows && (!k || !v)) || !cu_q || !cu_k || !out) return PQ2_ERR_NULL;
   if (dtype != PQ2_BF16 && dtype != PQ2_F16) return PQ2_ERR_DTYPE;
-  if (!valid_prefill(B, q_rows, k_rows, q_heads, heads, dim) || !is_finite(scale))
+  if (!valid_prefill(B, q_rows, k_rows, q_heads, heads, dim) || !valid_scale(scale))
     return PQ2_ERR_SHAPE;
   for (int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
                     v_head_stride}) {

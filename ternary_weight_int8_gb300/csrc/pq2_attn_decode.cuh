@@ -232,7 +232,7 @@ __device__ __forceinline__ float4 remote4(uint32_t addr) {
 }
 
 __device__ __forceinline__ int length(const Params& p, int b) {
-  return b < p.a.batch.B ? max(__ldg(p.a.batch.lens + b), 0) : 0;
+  return b < p.a.batch.B ? min(max(__ldg(p.a.batch.lens + b), 0), 1 << 30) : 0;
 }
 __device__ __forceinline__ int tiles_of(int len, int tile) {
   return max(1, len / tile + (len % tile != 0));

@@ -810,6 +810,13 @@ def pq2_kv_load(cache: KVCache, table, lens, cu=None, tokens=None, out=None,
 _attn_bytes = {}
 
 
+def _workspace(nbytes, like, stream):
+    w = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None and w.is_cuda:
+        w.record_stream(stream)  # it is let go of before the work on that stream is done
+    return w
+
+
 def _attn_outputs(q, out, lse):
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"Expected a bfloat16 or float16 tensor, not {q.dtype}")
@@ -847,9 +854,11 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
         key = (B, T, shape[-2], kv_heads, dim, width * cache.k.shape[2])
         nbytes = _attn_bytes.get(key)
         if nbytes is None:
+            if len(_attn_bytes) > 4096:
+                _attn_bytes.clear()
             nbytes = _attn_bytes[key] = L.pq2_attn_decode_workspace_bytes(*key)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _workspace(nbytes, q, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _on_one_device(q, *cache, table, lens, out, lse, workspace, status)
@@ -883,11 +892,10 @@ def pq2_attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal: bool = True, 
     keys, kv_heads, B = k_shape[0], k_shape[1], cu_q.shape[0] - 1
     if 1 in q_shape or 1 in k_shape:
         qs, ks, vs = _strides(q), _strides(k), _strides(v)
-    nbytes = 0
     if workspace is None:
         nbytes = lib().pq2_attn_prefill_workspace_bytes(B, rows, keys, heads, kv_heads, dim)
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        if nbytes:
+            workspace = _workspace(nbytes, q, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _on_one_device(q, k, v, cu_q, cu_k, out, lse, workspace, status)

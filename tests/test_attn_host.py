@@ -96,7 +96,7 @@ def test_decode_refusals(L):
     refused(L.pq2_attn_decode, ok, (0, None, NULL), (9, None, NULL), (12, None, NULL),
             (14, None, NULL), (16, None, NULL), (1, pq2.PQ2_F32, DTYPE), (1, 7, DTYPE),
             (5, 0, SHAPE), (5, 65537, SHAPE), (6, 0, SHAPE), (6, 65, SHAPE), (7, 3, SHAPE),
-            (7, 1024, SHAPE), (7, 0, SHAPE), (13, float("inf"), SHAPE), (13, float("nan"), SHAPE),
+            (7, 1024, SHAPE), (7, 0, SHAPE), (13, float("inf"), SHAPE), (13, 2e6, SHAPE), (13, float("nan"), SHAPE),
             (2, -2, SHAPE), (4, 127, ALIGN), (10, 3, SHAPE), (11, 0, SHAPE), (17, 0, SHAPE),
             (0, A + 2, ALIGN), (14, A + 8, ALIGN), (15, A + 2, ALIGN), (16, A + 8, ALIGN),
             (18, A + 1, ALIGN))
@@ -116,7 +116,7 @@ def test_prefill_refusals(L):
             (15, None, NULL), (16, None, NULL), (20, None, NULL), (9, pq2.PQ2_F32, DTYPE),
             (10, 0, SHAPE), (11, -1, SHAPE), (10, (1 << 24) + 1, SHAPE), (12, 5, SHAPE),
             (12, 258, SHAPE), (13, 0, SHAPE), (14, 32, SHAPE), (17, 0, SHAPE),
-            (18, float("nan"), SHAPE), (1, -8, SHAPE), (5, 1 << 39, SHAPE), (1, 508, ALIGN),
+            (18, float("nan"), SHAPE), (18, -2e6, SHAPE), (1, -8, SHAPE), (5, 1 << 39, SHAPE), (1, 508, ALIGN),
             (8, 4, ALIGN), (0, A + 8, ALIGN), (3, A + 2, ALIGN), (20, A + 8, ALIGN),
             (21, A + 1, ALIGN), (15, A + 2, ALIGN))
     f = L.pq2_attn_prefill_workspace_bytes

@@ -137,6 +137,43 @@ def test_what_is_not_seen_in_parts(D, bad):
     assert bool(pq2.pq2_attn_prefill(q, k, v, sums(nq), sums(nk))[:60].isnan().all())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_no_keys_at_all(D):
+    q, k, v = inputs([5, 3], [0, 0], 2, 3, D, BF16, seed=1)
+    assert k.shape[0] == 0
+    out = check(q, k, v, [5, 3], [0, 0])
+    assert not out.any()
+
+
+@pytest.mark.parametrize("nk", [60, 9000])
+def test_rows_before_the_first_sequence(nk):
+    """Sums that begin above 0: those rows stay as they were, with keys in one part
+    and in several."""
+    q, k, v = inputs([40], [nk], 2, 2, 128, BF16, seed=1)
+    want = pq2.pq2_attn_prefill(q[7:], k[9:], v[9:], sums([33]), sums([nk - 9]))
+    out = torch.full_like(q, float("nan"))
+    cu_q, cu_k = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([7, 40], [9, nk]))
+    pq2.pq2_attn_prefill(q, k, v, cu_q, cu_k, out=out)
+    assert bool(out[:7].isnan().all())
+    tol = 2.0 ** -7 * float(v.float().abs().max())
+    assert float((out[7:].float() - want.float()).abs().max()) <= tol
+
+
+def test_a_stream_given_by_name():
+    nq, nk = [40], [9000]
+    q, k, v = inputs(nq, nk, 2, 2, 128, BF16, seed=1)
+    want = pq2.pq2_attn_prefill(q, k, v, sums(nq), sums(nk))
+    torch.cuda.synchronize()
+    side, cu = torch.cuda.Stream(), (sums(nq), sums(nk))
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(q) for _ in range(8)]
+    for out in outs:  # the workspaces are let go of while that stream still uses them
+        pq2.pq2_attn_prefill(q, k, v, *cu, out=out, stream=side)
+        torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for out in outs)
+
+
 def test_a_workspace_of_the_callers():
     nq, nk = [50, 9], [9000, 5000]
     q, k, v = inputs(nq, nk, 2, 4, 128, F16, seed=2)

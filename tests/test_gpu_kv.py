@@ -172,6 +172,33 @@ def test_even_split_and_places_outside_the_cache():
     assert torch.equal(got[keep], k[keep]) and not got[~keep].any()
 
 
+def test_nothing_to_do():
+    cache = pq2.kv_cache(2, 2, 16, 64)
+    table = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    none = torch.empty((0, 2, 64), device="cuda")
+    pq2.pq2_kv_store(none, none, cache, table, ints([0]))
+    pq2.pq2_kv_store(none, none, cache, table, ints([5]), cu=ints([0, 0]))
+    k, v = pq2.pq2_kv_load(cache, table, ints([9]), tokens=0)
+    torch.cuda.synchronize()
+    assert k.shape == v.shape == (0, 2, 64) and not cache.k.any()
+
+
+def test_rows_outside_the_sequences():
+    """Sums that begin above 0 and end before the last row."""
+    cache = pq2.kv_cache(4, 2, 16, 64, BF16)
+    table = torch.tensor([[1, 3], [0, -1]], dtype=torch.int32, device="cuda")
+    x = torch.randn((20, 2, 64), generator=A.gen(1), device="cuda").bfloat16()
+    x[:3], x[16:] = float("nan"), float("nan")
+    cu, lens = ints([3, 13, 16]), ints([20, 3])
+    pq2.pq2_kv_store(x, -x, cache, table, lens, cu=cu)
+    out = [torch.full((20, 2, 64), 7.0, dtype=F32, device="cuda") for _ in range(2)]
+    pq2.pq2_kv_load(cache, table, lens, cu=cu, out=out)
+    assert torch.equal(out[0][3:16], x[3:16].float()) and torch.equal(out[1][3:16], -x[3:16].float())
+    for y in out:
+        assert bool((y[:3] == 7).all()) and bool((y[16:] == 7).all())
+    assert not cache.k.isnan().any() and not cache.v.isnan().any()
+
+
 def test_what_is_not_finite_reads_back_as_nan():
     k = torch.ones((3, 2, 128), device="cuda")
     k[0, 0, 5], k[1, 1, 7], k[2, 0, 0] = float("inf"), float("nan"), -float("inf")
