@@ -56,12 +56,7 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // how far m may stay behind, in powers of two
 constexpr int kBlock = 8;       // query rows of an MMA
 constexpr int kMaxCtas = 160;   // the SMs of the largest sm_103 device
-// Few items in short contexts: a cluster of 8 CTAs takes each and joins its
-// parts through distributed shared memory.  One launch and no workspace: 1 x 1024
-// tokens, 8 key heads of 128, bf16 6.6 against 8.3 us (8 bits 9.6 against 10.6),
-// and 13.8 against 21 us with the host's part.  Two such clusters fit a GPC, so
-// 16 items run at once; in longer contexts all SMs are worth more.
-constexpr int kCluster = 8, kClusterItems = 16, kClusterPositions = 4096;
+constexpr int kCluster = 8;     // CTAs that share an item at most, without a workspace
 constexpr int kScaleBytes = 128;  // of 16 scales: a copy's target is 128-byte aligned
 
 // A warp has NB blocks of 8 rows.  RT warps share a slice of tokens, each with
@@ -352,13 +347,13 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
   Cursor here;
   int parts = 1, rank = 0;  // of a cluster's item
   if (p.cluster) {
-    const int of = blockIdx.x / kCluster;
-    rank = blockIdx.x % kCluster;
+    const int of = blockIdx.x / p.cluster;
+    rank = blockIdx.x % p.cluster;
     here.b = of / p.items;
     here.head = of % p.items / p.row_groups, here.group = of % p.items % p.row_groups;
     here.len = length(p, here.b), here.next_len = 0;
     here.tiles = tiles_of(here.len, kTile);
-    parts = min(here.tiles, kCluster);
+    parts = min(here.tiles, p.cluster);
     here.tile = rank < parts ? (int)((int64_t)rank * here.tiles / parts) : 0;
     here.left = rank < parts ? (int)((int64_t)(rank + 1) * here.tiles / parts) - here.tile : 0;
     __syncthreads();
@@ -911,14 +906,14 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
       }
     }
   }
-  if (p.cluster) {
+  if (p.cluster > 1) {
     cluster_sync();
     if (parts > 1) {
-      const int of = blockIdx.x / kCluster, b = of / p.items;
+      const int of = blockIdx.x / p.cluster, b = of / p.items;
       const int head = of % p.items / p.row_groups, R0 = of % p.items % p.row_groups * G::rows;
       const int valid = min(G::rows, p.rows - R0), len = length(p, b);
       const float* part = reinterpret_cast<const float*>(smem);
-      for (int i = tid * kCluster + rank; i < valid * (D / 4); i += G::threads * kCluster) {
+      for (int i = tid * p.cluster + rank; i < valid * (D / 4); i += G::threads * p.cluster) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float m[kCluster], l[kCluster], m2[kCluster];
         float4 y[kCluster];
@@ -1046,7 +1041,7 @@ int launch(Params& p, int sm_count, cudaStream_t stream) {
     return PQ2_ERR_LAUNCH;
   p.row_groups = (p.rows + G::rows - 1) / G::rows;
   p.items = (int)p.cache.heads * p.row_groups;
-  const int ctas = p.cluster ? p.a.batch.B * p.items * kCluster : std::min(sm_count, kMaxCtas);
+  const int ctas = p.cluster ? p.a.batch.B * p.items * p.cluster : std::min(sm_count, kMaxCtas);
   p.places = reinterpret_cast<int4*>(p.a.workspace);
   p.parts = reinterpret_cast<float*>(p.a.workspace + kMaxCtas * sizeof(int4));
   cudaLaunchConfig_t cfg = {};
@@ -1058,9 +1053,9 @@ int launch(Params& p, int sm_count, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {kCluster, 1, 1};
+  attr[1].val.clusterDim = {(unsigned)p.cluster, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = p.cluster ? 2 : 1;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, mk, mv, mks, mvs, p) != cudaSuccess) {
     cudaGetLastError();
     return PQ2_ERR_LAUNCH;

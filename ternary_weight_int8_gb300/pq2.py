@@ -817,6 +817,25 @@ def _workspace(nbytes, like, stream):
     return w
 
 
+_kept = threading.local()  # .by: {(device, stream): a workspace of this thread's calls on it}
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
+
+
+def _kept_workspace(nbytes, like, stream):
+    """pq2_attn_decode's: a few MB, kept, as allocating them costs more than the
+    launch.  A thread's calls on one stream follow one another; another thread's
+    may come between a call's two kernels.  A captured graph may be replayed
+    anywhere, beside other graphs: it gets one of its own."""
+    if stream is not None or not like.is_cuda or _capturing is None or _capturing():
+        return _workspace(nbytes, like, stream)
+    by = _kept.__dict__.setdefault("by", {})
+    key = like.device, _stream(None)
+    w = by.get(key)
+    if w is None or w.numel() < nbytes:
+        w = by[key] = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return w
+
+
 def _attn_outputs(q, out, lse):
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"Expected a bfloat16 or float16 tensor, not {q.dtype}")
@@ -835,7 +854,8 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
     holds their keys and values already: q [B][heads][dim] or [B][T][heads][dim]
     -> out of q's shape.  Token t of T sees the positions before
     lens[b] - T + t + 1.  scale: 1 / sqrt(dim) if None; lse: a float32 buffer of
-    q.shape[:-1] for the rows' log-sum-exp."""
+    q.shape[:-1] for the rows' log-sum-exp; workspace: if None, one that is kept
+    per thread and stream (a captured call, or one with stream, gets its own)."""
     L = lib()
     c, kv_heads, dim = _c_cache(cache)
     shape, st = q.shape, q.stride()
@@ -858,7 +878,7 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
                 _attn_bytes.clear()
             nbytes = _attn_bytes[key] = L.pq2_attn_decode_workspace_bytes(*key)
         if nbytes:
-            workspace = _workspace(nbytes, q, stream)
+            workspace = _kept_workspace(nbytes, q, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _on_one_device(q, *cache, table, lens, out, lse, workspace, status)

@@ -91,7 +91,7 @@ def test_store_and_load_refusals(L):
 
 def test_decode_refusals(L):
     c = c_cache()
-    ok = [A, pq2.PQ2_BF16, 512, 512, 128, 9, 1, 4, ctypes.addressof(c), A, 4, 4, A, 1.0, A, A, A,
+    ok = [A, pq2.PQ2_BF16, 512, 512, 128, 9, 1, 4, ctypes.addressof(c), A, 10000, 10000, A, 1.0, A, A, A,
           1 << 40, A, None]
     refused(L.pq2_attn_decode, ok, (0, None, NULL), (9, None, NULL), (12, None, NULL),
             (14, None, NULL), (16, None, NULL), (1, pq2.PQ2_F32, DTYPE), (1, 7, DTYPE),
@@ -101,8 +101,9 @@ def test_decode_refusals(L):
             (0, A + 2, ALIGN), (14, A + 8, ALIGN), (15, A + 2, ALIGN), (16, A + 8, ALIGN),
             (18, A + 1, ALIGN))
     f = L.pq2_attn_decode_workspace_bytes
-    assert f(1, 1, 4, 2, 128, 4096) == 0 and f(16, 1, 8, 1, 128, 4096) == 0
-    for some in ((1, 1, 4, 2, 128, 4112), (17, 1, 8, 1, 64, 16), (1, 5, 320, 8, 64, 16)):
+    for none in ((1, 1, 4, 2, 128, 4096), (16, 1, 8, 1, 128, 4096), (1, 5, 320, 8, 64, 16)):
+        assert f(*none) == 0
+    for some in ((1, 1, 4, 2, 128, 1 << 17), (300, 1, 8, 2, 128, 256), (64, 1, 32, 8, 64, 16384), (2, 8, 64, 8, 256, 40000)):
         assert f(*some) > 0
     for bad in ((0, 1, 4, 2, 128, 1 << 20), (1, 0, 4, 2, 128, 1 << 20), (1, 1, 3, 2, 128, 1 << 20),
                 (1, 1, 4, 2, 80, 1 << 20), (1, 1, 514, 2, 64, 1 << 20), (99, 1, 4, 2, 128, -1)):

@@ -1,5 +1,6 @@
 """pq2_attn_decode against the definition in 64 bits (bounds in attn_util)."""
 import math
+import threading
 
 import pytest
 import torch
@@ -250,6 +251,67 @@ def test_three_dimensions_streams_and_a_captured_graph():
         verify(out, None, static_q, cache, new, short)
 
 
+@pytest.mark.parametrize("B,H,G,T", [(1, 1, 1, 1), (3, 5, 4, 1), (9, 4, 3, 1), (20, 3, 6, 1),
+                                     (40, 2, 5, 4), (90, 2, 16, 1), (60, 8, 2, 2)])
+@pytest.mark.parametrize("cache_dtype", [BF16, I8])
+def test_short_tables(B, H, G, T, cache_dtype):
+    """From one item to several for every SM: clusters of 8, 4, 2 and 1, and, where
+    the items would take them four rounds (480), even shares."""
+    lens = [(13 * b * b + 5 * b) % 257 for b in range(B)]
+    cache, table, dense = A.make_cache(B, lens, H, 16, 128, cache_dtype, seed=B, width=17)
+    nbytes = pq2.lib().pq2_attn_decode_workspace_bytes(B, T, H * G, H, 128, 17 * 16)
+    assert (nbytes > 0) == (B * H == 480)
+    check(queries(B, T, H * G, 128, BF16, seed=G), cache, table, lens, dense)
+
+
+def test_graphs_replayed_at_once():
+    """Two graphs of one stream, with workspaces, replayed on two streams."""
+    lens = [9000, 4000, 77]
+    cache, table, dense = A.make_cache(3, lens, 2, 16, 128, I8, seed=2, width=20000)
+    n = ints(lens)
+    qs = [queries(3, 1, 8, 128, BF16, seed=s) for s in (1, 2)]
+    want = [check(q, cache, table, lens, dense) for q in qs]
+    graphs, outs = [], []
+    for q in qs:
+        outs.append(torch.empty_like(q))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(20):
+                pq2.pq2_attn_decode(q, cache, table, n, out=outs[-1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s, o in zip(graphs, streams, outs):
+            with torch.cuda.stream(s):
+                o.zero_()
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_two_threads_on_one_stream():
+    """Each call's workspace is its own until its second kernel has run."""
+    lens = [9000, 4000, 77]
+    cache, table, dense = A.make_cache(3, lens, 2, 16, 128, I8, seed=2, width=20000)
+    n = ints(lens)
+    qs = [queries(3, 1, 8, 128, BF16, seed=s) for s in (1, 2)]
+    want = [check(q, cache, table, lens, dense) for q in qs]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def calls(i):
+        got[i] = [pq2.pq2_attn_decode(qs[i], cache, table, n) for _ in range(200)]
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for some, w in zip(got, want):
+        assert some and all(torch.equal(o, w) for o in some)
+
+
 def test_offsets_beyond_32_bits():
     """A pool whose pages lie more than 2^31 elements apart."""
     D, page, n = 64, 16, 40
@@ -268,7 +330,11 @@ def test_a_workspace_of_the_callers():
     lens = [4500, 2]
     cache, table, dense = A.make_cache(2, lens, 2, 16, 128, F16, seed=2)
     q = queries(2, 1, 10, 128, F16, seed=1)
+    wide = torch.full((2, 4000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    table = wide
     nbytes = pq2.lib().pq2_attn_decode_workspace_bytes(2, 1, 10, 2, 128, 16 * table.shape[1])
+    assert nbytes
     back = torch.full((nbytes + 512,), 0x5A, dtype=torch.uint8, device="cuda")
     check(q, cache, table, lens, dense, workspace=back[256:256 + nbytes])
     assert bool((back[:256] == 0x5A).all()) and bool((back[256 + nbytes:] == 0x5A).all())
@@ -281,13 +347,15 @@ def test_a_workspace_of_the_callers():
 @pytest.mark.parametrize("lens,H,G,T", [([4096], 8, 5, 1), ([4000, 0, 1, 700], 4, 3, 1),
                                         ([1, 2, 3, 2000, 513], 3, 6, 4), ([1025], 1, 8, 7)])
 def test_a_wider_table_changes_nothing(dtype, cache_dtype, D, lens, H, G, T):
-    """Short tables run in clusters, longer ones in even shares of the SMs: both
-    against 64 bits, and within two roundings of each other."""
+    """Short tables run in clusters of 1 to 8 CTAs, long ones in even shares of the
+    SMs: all against 64 bits, and within two roundings of each other."""
     B = len(lens)
     cache, table, dense = A.make_cache(B, lens, H, 32, D, cache_dtype, seed=D + T, width=128)
     q = queries(B, T, H * G, D, dtype, seed=4)
-    wide = torch.full((B, 200), -3, dtype=torch.int32, device="cuda")
-    wide[:, :128] = table
     a = check(q, cache, table, lens, dense)
-    b = check(q, cache, wide, lens, dense)
-    assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -6 * float(a.float().abs().max())
+    for width in (300, 1000, 10000):
+        wide = torch.full((B, width), -3, dtype=torch.int32, device="cuda")
+        wide[:, :128] = table
+        b = check(q, cache, wide, lens, dense)
+        assert float((a.float() - b.float()).abs().max()) <= \
+            2.0 ** -6 * float(a.float().abs().max())
