@@ -740,12 +740,13 @@ int pq2_kv_load(const pq2_kv_cache *cache, const int32_t *table,
  *   workspace (device) pq2_attn_decode_workspace_bytes (positions =
  *            table_width * page_size), 16-byte aligned; NULL where that is 0.
  *            Its contents need not be kept between calls.  Calls that may run
- *            at the same time need one each.
+ *            at the same time, or that two threads make on one stream (a call
+ *            may launch two kernels), need one each.
  * Scores, the softmax and all sums are fp32.  The weights are rounded to the
  * type in which the tensor cores take them (a 16-bit cache: q's; an 8-bit one:
  * fp16), keys and values not at all.  The order of the sums follows B, T,
- * lens, the heads and the SM count; the same call gives the same bits.
- * pq2_attn_decode_workspace_bytes returns 0 for few heads and short tables,
+ * lens, table_width, the heads and the SM count; the same call gives the same bits.
+ * pq2_attn_decode_workspace_bytes returns 0 for short tables and few sequences,
  * which need none, and for invalid arguments. */
 size_t pq2_attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads,
                                        int64_t heads, int64_t dim,
