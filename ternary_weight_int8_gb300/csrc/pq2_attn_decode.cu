@@ -8,7 +8,9 @@ namespace pq2 {
 namespace {
 
 // Rows of a CTA, as launch_rows chooses them.
-int group_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int group_rows(int64_t rows, int64_t dim) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 && dim == 256 ? 24 : 32;
+}
 // How many CTAs take an item together, in a cluster that joins its parts through
 // distributed shared memory, or one alone; 0: even shares of all SMs, which need a
 // workspace and a second kernel.  The table bounds the lengths.  An SM begins in
@@ -21,7 +23,7 @@ int group_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 // 4 against 9.8 (16); 8 x 1500 9.9 (11.1) in clusters of 2 against 11.3 (16); 16 x 700
 // 8.6 (11.1) alone against 12.5 (16); 1 x 8192 11.0 (12.0) against 10.3 (16).
 int cluster_of(int64_t B, int64_t rows, int64_t heads, int64_t dim, int64_t positions) {
-  const int n = group_rows(rows);
+  const int n = group_rows(rows, dim);
   const int64_t items = B * heads * ((rows + n - 1) / n);
   const double bytes = (double)positions * (double)dim * 4;  // of an item, 16 bits
   double least = (double)items * bytes / 2 / 6.7e6 + 14;
@@ -40,7 +42,7 @@ size_t attn_decode_workspace_bytes(int64_t B, int64_t T, int64_t q_heads, int64_
                                    int64_t dim, int64_t positions) {
   const int64_t rows = T * (q_heads / heads);
   if (cluster_of(B, rows, heads, dim, positions)) return 0;
-  return kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * group_rows(rows) * (dim + 3) * sizeof(float);
+  return kMaxCtas * sizeof(int4) + (size_t)2 * kMaxCtas * group_rows(rows, dim) * (dim + 3) * sizeof(float);
 }
 
 int launch_attn_decode(const DecodeParams& a, const pq2_kv_cache& c, int sm_count,

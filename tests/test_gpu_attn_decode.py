@@ -264,6 +264,20 @@ def test_short_tables(B, H, G, T, cache_dtype):
     check(queries(B, T, H * G, 128, BF16, seed=G), cache, table, lens, dense)
 
 
+@pytest.mark.parametrize("T,G", [(17, 1), (3, 6), (4, 6), (5, 5), (2, 23)])
+@pytest.mark.parametrize("q_dtype,cache_dtype", [(BF16, BF16), (F16, F16), (F16, I8), (BF16, I8)])
+def test_rows_of_256(T, G, q_dtype, cache_dtype):
+    """17 to 24 rows and the first above, in clusters and in even shares."""
+    lens = [0, T - 1, 100, 1333, 3000]
+    cache, table, dense = A.make_cache(5, lens, 2, 16, 256, cache_dtype, seed=T)
+    q = queries(5, T, 2 * G, 256, q_dtype, seed=G)
+    check(q, cache, table, lens, dense)
+    wide = torch.full((5, 10000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    assert pq2.lib().pq2_attn_decode_workspace_bytes(5, T, 2 * G, 2, 256, 160000)
+    check(q, cache, wide, lens, dense)
+
+
 def test_graphs_replayed_at_once():
     """Two graphs of one stream, with workspaces, replayed on two streams."""
     lens = [9000, 4000, 77]
