@@ -11,14 +11,16 @@
 // transposed, as their 16 rows and 8 query rows as their columns (scores^T = K
 // Q^T, out^T = V^T W^T), so that few rows leave little of them empty.
 //
-// Work is cut evenly whatever the lengths: the tiles of 16 * warps tokens of
+// Work is cut evenly whatever the lengths: the tiles of 64 to 384 tokens of
 // all (sequence, key head, row tile) are numbered, and a CTA takes a
 // contiguous share of them, which may end inside a sequence and span several.
-// Inside a tile each warp has 16 tokens of its own, which it copies itself
+// Inside a tile each warp has 16 or 32 tokens of its own, which it copies itself
 // (tensor-map boxes of 16 slots into a ring that no other warp touches, so
-// nothing waits for another warp before the join) and folds into sums of its
+// nothing waits for another warp before the join; many rows of 256 columns: two
+// or three warps with rows of their own share them) and folds into sums of its
 // own.  At the end of a CTA's part of a sequence the warps join; parts that
-// are not whole go to the workspace, and a second kernel joins them.
+// are not whole go to the workspace, and a second kernel joins them.  Short tables
+// with few items: a CTA or a cluster an item, joined in distributed shared memory.
 //
 // 8-bit caches: codes become fp16 by byte permutes (0x6400 | code + 128 is
 // 1024 + 128 + code) and one exact subtraction.  A key's scale multiplies its
@@ -1078,7 +1080,7 @@ int launch_rows(Params& p, int sm_count, cudaStream_t stream) {
   if (p.rows <= 16) return launch<QT, CT, D, 1, 2>(p, sm_count, stream);
   // 32 rows of 256 columns are more than a thread's registers.  24 are three warps'
   // of 8, with twelve warps an SM instead of eight of 16: 12 ragged sequences of up
-  // to 6000, 24 rows, 39.5 -> 36.3 us (equal ones 62.2 -> 60.6).  24 rows of 128
+  // to 6000, 24 rows, 39.5 -> 36.3 us (equal ones 62.2 -> 60.6).  20 rows of 128
   // columns: 92 us with eight warps of 32 rows, 97 so.
   if constexpr (D == 256) {
     if (p.rows <= 24) return launch<QT, CT, D, 3, 1>(p, sm_count, stream);
