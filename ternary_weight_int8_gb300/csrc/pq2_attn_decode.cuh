@@ -24,9 +24,10 @@
 //
 // 8-bit caches: codes become fp16 by byte permutes (0x6400 | code + 128 is
 // 1024 + 128 + code) and one exact subtraction.  A key's scale multiplies its
-// score; a value's goes into its weight, w_j = 2^(s_j + log2 scale_j - m2)
-// with a maximum m2 of its own, so that weights are at most 2^8 and keep their
-// bits whatever the scales are.
+// score; a value's goes into its weight, w_j = 2^(s_j - m - u) scale_j with a
+// unit 2^u of its own beside 2^m, so that weights are at most 2^8 and keep their
+// bits whatever the scales are.  u is held relative to m, as large maxima have no
+// bits for it.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -56,6 +57,10 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // how far m may stay behind, in powers of two
+// How far below 2^m the unit of an 8-bit cache's sums may lie: w_j's factors stay
+// finite, and what the sums lose when the unit moves up to there is below
+// 2^-149 of 2^(m - kLead).
+constexpr float kLead = 60.f;
 constexpr int kBlock = 8;       // query rows of an MMA
 constexpr int kMaxCtas = 160;   // the SMs of the largest sm_103 device
 constexpr int kCluster = 8;     // CTAs that share an item at most, without a workspace
@@ -120,6 +125,13 @@ __device__ __forceinline__ float lg2(float x) {
 // 2^(m - top), 0 for the maximum of nothing.
 __device__ __forceinline__ float weight(float m, float top) {
   return m == -INFINITY ? 0.f : ex2(m - top);
+}
+// The exponent of the unit of sums beside a maximum m, counted from M >= m: u over
+// an 8-bit cache, 0 over others; -infinity where nothing has been summed.
+template <typename CT>
+__device__ __forceinline__ float unit_from(float m, float u, float M) {
+  if (sizeof(CT) == 1) return u == -INFINITY ? u : m - M + u;
+  return m == -INFINITY ? m : m - M;
 }
 
 template <typename T> __device__ __forceinline__ uint32_t pack(float lo, float hi);
@@ -289,11 +301,11 @@ __device__ __noinline__ float4 plain_columns(const Params& p, int b, int kh, int
   return make_float4(o[0] / l, o[1] / l, o[2] / l, o[3] / l);
 }
 
-// Four columns of a joined row to out, and its lse: o in units of 2^m2, the
+// Four columns of a joined row to out, and its lse: o in units of 2^(m + u), the
 // weights' sum l in units of 2^m.
 template <typename QT, typename CT, int D>
 __device__ __forceinline__ void finish(const Params& p, int b, int kh, int R, int d, int len,
-                                       float4 o, float m, float l, float m2) {
+                                       float4 o, float m, float l, float u) {
   if (R >= p.rows) return;
   const int t = R / p.group, most = len - p.a.T + t + 1;
   const int64_t row =
@@ -301,7 +313,7 @@ __device__ __forceinline__ void finish(const Params& p, int b, int kh, int R, in
   if (most <= 0) {
     o = make_float4(0.f, 0.f, 0.f, 0.f);
   } else {
-    const float f = (sizeof(CT) == 1 ? weight(m2, m) : 1.f) / l;
+    const float f = (sizeof(CT) == 1 ? ex2(u) : 1.f) / l;
     o.x *= f, o.y *= f, o.z *= f, o.w *= f;
     const float zero = (o.x + o.y) * 0.f + (o.z + o.w) * 0.f;
     if (zero != 0.f && l - l == 0.f && most < len)
@@ -327,7 +339,7 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
   uint8_t* smem = smem_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
   float* join = reinterpret_cast<float*>(smem + G::offJoin);
   uint4* q_frag = reinterpret_cast<uint4*>(smem + G::offQ);
-  float* stat = reinterpret_cast<float*>(smem + G::offStat);  // m, l, m2 of [warp][row]
+  float* stat = reinterpret_cast<float*>(smem + G::offStat);  // m, l, u of [warp][row]
   constexpr int kWarpRows = G::warpRows;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + G::offBar);
 
@@ -617,12 +629,12 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][nb][e] = 0.f;
     float m[NB][2], l[NB][2];
-    float m2[NB][2], ratio[NB][2];  // 8-bit caches: m2, and 2^(m - m2)
+    float u[NB][2], ratio[NB][2];  // 8-bit caches: u, and 2^-u
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        m[nb][e] = m2[nb][e] = -INFINITY, l[nb][e] = 0.f, ratio[nb][e] = 1.f;
+        m[nb][e] = u[nb][e] = -INFINITY, l[nb][e] = 0.f, ratio[nb][e] = 1.f;
     const auto rescale = [&](const float (&f)[NB][2]) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -722,9 +734,14 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
           for (int e = 0; e < 2; ++e) {
             const float top = fmaxf(over_tokens(h[nb][e]), m[nb][e]);
             f[nb][e] = weight(m[nb][e], top);
-            m[nb][e] = top;
             l[nb][e] *= f[nb][e];
-            if (kEight && m2[nb][e] != -INFINITY) ratio[nb][e] = ex2(fminf(top - m2[nb][e], 126.f));
+            if (kEight && u[nb][e] != -INFINITY) {
+              // The sums keep their unit; where it lies too far below now, the
+              // weights are made for the lowest one and the sums scaled after them.
+              u[nb][e] -= top - m[nb][e];
+              ratio[nb][e] = ex2(fminf(-u[nb][e], kLead));
+            }
+            m[nb][e] = top;
           }
         if constexpr (!kEight) rescale(f);
       }
@@ -743,7 +760,7 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
       ok = ok && mbar_wait(&bar[st], used / G::depth & 1);
       from = ring + st * G::unit;
       if constexpr (kEight) {
-        // The same with the values' scales in the weights: 2^(s - m) v 2^(m - m2).
+        // The same with the values' scales in the weights: 2^(s - m) scale 2^-u.
         scales = reinterpret_cast<const float*>(scale_p + st * G::scale) + g;
         constexpr float kMost = 256.f;  // 2^kSlack
         bool up = false;
@@ -766,7 +783,7 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) up = up || h[nb][e] > kMost || m2[nb][e] == -INFINITY;
+          for (int e = 0; e < 2; ++e) up = up || h[nb][e] > kMost || u[nb][e] < -kLead;
         if (__any_sync(~0u, up)) {
           float f[NB][2];
 #pragma unroll
@@ -774,16 +791,15 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float top = over_tokens(h[nb][e]);
-              // Without an m2 yet the weights are in units of 2^m.
-              const bool none = m2[nb][e] == -INFINITY, to = top > (none ? 0.f : kMost);
-              const float k = to ? lg2(top) : 0.f;
-              if (to) {
-                m2[nb][e] = (none ? m[nb][e] : m2[nb][e]) + k;
-                ratio[nb][e] = ex2(fminf(m[nb][e] - m2[nb][e], 126.f));
-              }
-              f[nb][e] = ex2(-k);
+              // Without a unit yet the weights are in units of 2^m.
+              const bool none = u[nb][e] == -INFINITY, to = top > (none ? 0.f : kMost);
+              const float k = to ? lg2(top) : 0.f, low = none ? 0.f : fmaxf(u[nb][e], -kLead);
+              f[nb][e] = none ? 1.f : ex2(u[nb][e] - low - k);
+              if (to || !none) u[nb][e] = low + k;
+              if (to) ratio[nb][e] = ex2(-u[nb][e]);
+              const float by = ex2(-k);
 #pragma unroll
-              for (int t = 0; t < MT16; ++t) s[t][nb][e] *= f[nb][e], s[t][nb][e + 2] *= f[nb][e];
+              for (int t = 0; t < MT16; ++t) s[t][nb][e] *= by, s[t][nb][e + 2] *= by;
             }
           rescale(f);
         }
@@ -844,7 +860,7 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
           float* to = stat + warp * kWarpRows + nb * kBlock + 2 * i4 + e;
           to[0] = m[nb][e];
           to[W * kWarpRows] = sum;
-          to[2 * W * kWarpRows] = kEight ? m2[nb][e] : m[nb][e];
+          if (kEight) to[2 * W * kWarpRows] = u[nb][e];
         }
       }
     // On to the next item: its queries come in while this one is joined.
@@ -857,7 +873,7 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
     // Thread (r, x): row r, columns 4 x of every round; the warps that have it.
     constexpr int S = G::slices, kCols = G::joinCols, kQuads = kCols / 4;
     const int r = tid / kQuads, x4 = tid % kQuads * 4, w0 = r / kWarpRows * S;
-    float M = -INFINITY, M2 = -INFINITY, L = 0.f, f[S];
+    float M = -INFINITY, U = -INFINITY, L = 0.f, f[S];
 #pragma unroll
     for (int round = 0; round < D / kCols; ++round) {
       if (round) __syncthreads();
@@ -876,15 +892,15 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
         const float* st = stat + w0 * kWarpRows + r % kWarpRows;
         if (round == 0) {
 #pragma unroll
-          for (int w = 0; w < S; ++w) {
-            M = fmaxf(M, st[w * kWarpRows]);
-            M2 = fmaxf(M2, st[(2 * W + w) * kWarpRows]);
-          }
+          for (int w = 0; w < S; ++w) M = fmaxf(M, st[w * kWarpRows]);
 #pragma unroll
           for (int w = 0; w < S; ++w) {
             L += st[(W + w) * kWarpRows] * weight(st[w * kWarpRows], M);
-            f[w] = weight(st[(2 * W + w) * kWarpRows], M2);
+            f[w] = unit_from<CT>(st[w * kWarpRows], kEight ? st[(2 * W + w) * kWarpRows] : 0.f, M);
+            U = fmaxf(U, f[w]);
           }
+#pragma unroll
+          for (int w = 0; w < S; ++w) f[w] = weight(f[w], U);
         }
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -896,13 +912,13 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
         }
         const int d = round * kCols + x4;
         if (whole) {
-          finish<QT, CT, D>(p, b, head, R0 + r, d, len, sum, M, L, M2);
+          finish<QT, CT, D>(p, b, head, R0 + r, d, len, sum, M, L, U);
         } else {
           *reinterpret_cast<float4*>(part + r * D + d) = sum;
           if (d == 0) {
             part[G::rows * D + r] = M;
             part[G::rows * D + G::rows + r] = L;
-            part[G::rows * D + 2 * G::rows + r] = M2;
+            part[G::rows * D + 2 * G::rows + r] = U;
           }
         }
       }
@@ -917,28 +933,33 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
       const float* part = reinterpret_cast<const float*>(smem);
       for (int i = tid * p.cluster + rank; i < valid * (D / 4); i += G::threads * p.cluster) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float m[kCluster], l[kCluster], m2[kCluster];
+        float m[kCluster], l[kCluster], u[kCluster];
         float4 y[kCluster];
-        float M = -INFINITY, M2 = -INFINITY, L = 0.f;
+        float M = -INFINITY, U = -INFINITY, L = 0.f;
 #pragma unroll
         for (int k = 0; k < kCluster; ++k) {
-          m[k] = m2[k] = -INFINITY, l[k] = 0.f, y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          m[k] = u[k] = -INFINITY, l[k] = 0.f, y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k < parts) {
             const uint32_t at = map_rank(part, k), st = at + (G::rows * D + r) * 4;
-            m[k] = remote(st), l[k] = remote(st + G::rows * 4), m2[k] = remote(st + G::rows * 8);
+            m[k] = remote(st), l[k] = remote(st + G::rows * 4), u[k] = remote(st + G::rows * 8);
             y[k] = remote4(at + (r * D + d) * 4);
           }
-          M = fmaxf(M, m[k]), M2 = fmaxf(M2, m2[k]);
+          M = fmaxf(M, m[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) {
+          u[k] = unit_from<CT>(m[k], u[k], M);
+          U = fmaxf(U, u[k]);
         }
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kCluster; ++k) {
           L += l[k] * weight(m[k], M);
-          const float f = weight(m2[k], M2);
+          const float f = weight(u[k], U);
           sum.x = fmaf(y[k].x, f, sum.x), sum.y = fmaf(y[k].y, f, sum.y);
           sum.z = fmaf(y[k].z, f, sum.z), sum.w = fmaf(y[k].w, f, sum.w);
         }
-        finish<QT, CT, D>(p, b, head, R0 + r, d, len, sum, M, L, M2);
+        finish<QT, CT, D>(p, b, head, R0 + r, d, len, sum, M, L, U);
       }
     }
     cluster_sync();  // until all have read this CTA's part
@@ -962,36 +983,29 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   const auto part = [&](int i) {
     return p.parts + (size_t)(2 * (to.z + i) + (i == 0)) * G::slot;
   };
-  float M = -INFINITY, M2 = -INFINITY, L = 0.f;
+  float M = -INFINITY, U = -INFINITY, L = 0.f;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](float4 y, float m, float l, float u) {
+    const float top = fmaxf(M, m), now = unit_from<CT>(M, U, top), more = unit_from<CT>(m, u, top);
+    L = L * weight(M, top) + l * weight(m, top);
+    M = top, U = fmaxf(now, more);
+    const float a = weight(now, U), e = weight(more, U);
+    sum.x = sum.x * a + y.x * e, sum.y = sum.y * a + y.y * e;
+    sum.z = sum.z * a + y.z * e, sum.w = sum.w * a + y.w * e;
+  };
   for (int i = share; i < to.w; i += kSplit) {
     const float* from = part(i);
     const float m = from[G::rows * D + r], l = from[G::rows * D + G::rows + r],
-                m2 = from[G::rows * D + 2 * G::rows + r];
-    const float4 y = *reinterpret_cast<const float4*>(from + r * D + col * 4);
-    const float top = fmaxf(M, m), top2 = fmaxf(M2, m2);
-    L = L * weight(M, top) + l * weight(m, top);
-    const float a = weight(M2, top2), e = weight(m2, top2);
-    sum.x = sum.x * a + y.x * e, sum.y = sum.y * a + y.y * e;
-    sum.z = sum.z * a + y.z * e, sum.w = sum.w * a + y.w * e;
-    M = top, M2 = top2;
+                u = from[G::rows * D + 2 * G::rows + r];
+    add(*reinterpret_cast<const float4*>(from + r * D + col * 4), m, l, u);
   }
   sums[share][col] = sum;
-  if (col == 0) stats[share][0] = M, stats[share][1] = L, stats[share][2] = M2;
+  if (col == 0) stats[share][0] = M, stats[share][1] = L, stats[share][2] = U;
   __syncthreads();
   if (share) return;
-  for (int i = 1; i < kSplit; ++i) {
-    const float m = stats[i][0], l = stats[i][1], m2 = stats[i][2];
-    const float4 y = sums[i][col];
-    const float top = fmaxf(M, m), top2 = fmaxf(M2, m2);
-    L = L * weight(M, top) + l * weight(m, top);
-    const float a = weight(M2, top2), e = weight(m2, top2);
-    sum.x = sum.x * a + y.x * e, sum.y = sum.y * a + y.y * e;
-    sum.z = sum.z * a + y.z * e, sum.w = sum.w * a + y.w * e;
-    M = top, M2 = top2;
-  }
+  for (int i = 1; i < kSplit; ++i) add(sums[i][col], stats[i][0], stats[i][1], stats[i][2]);
   finish<QT, CT, D>(p, to.x, to.y / p.row_groups, to.y % p.row_groups * G::rows + r, col * 4,
-                    length(p, to.x), sum, M, L, M2);
+                    length(p, to.x), sum, M, L, U);
 }
 
 // ------------------------------------------------------------------- host

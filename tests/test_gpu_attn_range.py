@@ -1,0 +1,101 @@
+"""The attention and the cache at the ends of their ranges (bounds in attn_util)."""
+import math
+
+import pytest
+import torch
+
+from ternary_weight_int8_gb300 import pq2
+import attn_util as A
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32, I8 = A.BF16, A.F16, A.F32, A.I8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pq2.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def table_of(pages, width):
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, :pages] = torch.arange(pages, dtype=torch.int32)
+    return table
+
+
+def decode_and_check(q, k, v, cache_dtype, scale=1.0, wide=(False, True)):
+    """One sequence of n keys k and values v [n][H][D] (fp32) through a cache, q
+    [1][T][Hq][D] over it, against 64 bits: bounds of attn_util, where over 8 bits
+    the weights' unit is at most the largest exp(s_j) times value scale of a row
+    or, where that is less, 2^-60 exp(m).  Weights below 2^-126 are zero."""
+    n, H, D = k.shape
+    T, Hq = q.shape[1:3]
+    G = Hq // H
+    pages = -(-n // 16)
+    cache = pq2.kv_cache(pages, H, 16, D, cache_dtype)
+    table = table_of(pages, pages)
+    pq2.pq2_kv_store(k, v, cache, table, ints([n]))
+    dense = [x.double().transpose(0, 1)
+             for x in pq2.pq2_kv_load(cache, table, ints([n]), tokens=n, out_dtype=F32)]
+    for w in wide:
+        lse = torch.empty(q.shape[:-1], device="cuda")
+        out = pq2.pq2_attn_decode(q, cache, table_of(pages, 10000 if w else pages), ints([n]),
+                                  scale=scale, lse=lse)
+        assert not w or pq2.lib().pq2_attn_decode_workspace_bytes(1, T, Hq, H, D, 160000)
+        most = (n - T + 1 + torch.arange(T, device="cuda")).repeat_interleave(G)
+        for h in sorted({0, H // 3, H - 1}):
+            at = slice(h * G, h * G + G)
+            rows, kk, vv = q[0, :, at].double().reshape(T * G, D), dense[0][h], dense[1][h]
+            ref = A.attend(rows, kk, vv, most, scale)
+            small = None
+            if cache_dtype == I8:
+                unit = cache.v_scales.view(pages, H, 16)[:, h].reshape(-1)[:n].double()
+                seen = torch.arange(n, device="cuda")[None, :] < most[:, None]
+                z = torch.where(seen, rows @ kk.t() * scale, -math.inf)
+                e = torch.exp(z - z.amax(1, keepdim=True))
+                largest = (e * unit).amax(1) + 2.0 ** -60
+                small = (2 * 127 * n * largest)[:, None]
+            else:
+                small = ref[3]
+            # what weights that are flushed to zero leave out
+            small = small + 2.0 ** (25 - 117) * ref[3]
+            A.check_rows(out[0, :, at].reshape(T * G, D), lse[0, :, at].reshape(T * G), ref, D,
+                         F16 if cache_dtype == I8 else q.dtype, small)
+
+
+def queries(T, Hq, D, dtype):
+    q = torch.zeros((1, T, Hq, D), dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([1.0, 0.5, -1.0, 0.0], device="cuda").repeat(Hq // 4 + 1)[:Hq]
+    return q
+
+
+def keys_of(sizes, D, H=1):
+    """Keys with these scores under a query of one."""
+    k = torch.zeros((len(sizes), H, D), device="cuda")
+    k[..., 0] = sizes.float()[:, None]
+    return k
+
+
+@pytest.mark.parametrize("q_dtype,cache_dtype", [(BF16, I8), (F16, I8), (BF16, BF16)])
+@pytest.mark.parametrize("D,T,G", [(128, 1, 4), (64, 4, 5), (256, 4, 6), (256, 1, 32)])
+@pytest.mark.parametrize("n,H", [(700, 1), (2500, 100)])
+@pytest.mark.parametrize("rise", [84, 86, 100, 300, 1000])
+@pytest.mark.parametrize("order", ["late", "rising", "steps"])
+def test_scores_that_rise_far(q_dtype, cache_dtype, D, T, G, n, H, rise, order):
+    """A row's maximum rises by more than fp32 has powers of two, at the end, with
+    every key or between slices: of several warps or CTAs (one head), and of one
+    warp that has seen the keys before (many)."""
+    j = torch.arange(n, device="cuda")
+    size = {"late": torch.where(j == n - T, float(rise), 0.0), "rising": j / n * rise,
+            "steps": (j // (n // 7)) * (rise / 7)}[order]
+    for spread in (1.0, 400.0):  # value scales near 0.02 and 8
+        v = torch.randn((n, H, D), generator=A.gen(8), device="cuda") * spread
+        decode_and_check(queries(T, G * H, D, q_dtype), keys_of(size, D, H), v, cache_dtype)
