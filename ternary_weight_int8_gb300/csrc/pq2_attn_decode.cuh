@@ -57,10 +57,10 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;   // how far m may stay behind, in powers of two
-// How far below 2^m the unit of an 8-bit cache's sums may lie: w_j's factors stay
+// How far below 2^m the unit of an 8-bit cache's sums may lie: 2^(s_j - m - u) stays
 // finite, and what the sums lose when the unit moves up to there is below
 // 2^-149 of 2^(m - kLead).
-constexpr float kLead = 60.f;
+constexpr float kLead = 118.f;
 constexpr int kBlock = 8;       // query rows of an MMA
 constexpr int kMaxCtas = 160;   // the SMs of the largest sm_103 device
 constexpr int kCluster = 8;     // CTAs that share an item at most, without a workspace
@@ -189,6 +189,12 @@ __device__ __forceinline__ uint4 ldsm_t(uint32_t addr) {
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// The larger one, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 // Codes x and y (bytes X and Y of u, already 128 above) as fp16 pairs.
@@ -759,10 +765,19 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
       st = used % G::depth;
       ok = ok && mbar_wait(&bar[st], used / G::depth & 1);
       from = ring + st * G::unit;
+      uint2 w[MT16][NB];  // the weights, two tokens' a word
       if constexpr (kEight) {
-        // The same with the values' scales in the weights: 2^(s - m) scale 2^-u.
+        // The same with the values' scales in the weights: 2^(s - m) scale 2^-u, first in
+        // the units as they are.
         scales = reinterpret_cast<const float*>(scale_p + st * G::scale) + g;
         constexpr float kMost = 256.f;  // 2^kSlack
+        // What a row does not see may have any scale.
+        const auto unseen = [&](int t, int nb, int e) {
+          return edge && token + 16 * t + g + e / 2 * 8 >= most[nb][e & 1];
+        };
+        const auto scaled = [&](int t, int nb, int e, float by) {
+          return unseen(t, nb, e) ? 0.f : s[t][nb][e] * ratio[nb][e & 1] * by;
+        };
         bool up = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) h[nb][0] = h[nb][1] = 0.f;
@@ -770,38 +785,71 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
         for (int t = 0; t < MT16; ++t) {
           const float va = scales[t * (kScaleBytes / 4)], vb = scales[t * (kScaleBytes / 4) + 8];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb) {
+            float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = s[t][nb][e] * ((e < 2 ? va : vb) * ratio[nb][e & 1]);
-              // What a row does not see may have any scale.
-              if (edge && token + 16 * t + g + e / 2 * 8 >= most[nb][e & 1]) x = 0.f;
-              s[t][nb][e] = x;
-              h[nb][e & 1] = fmaxf(h[nb][e & 1], x);
+              x[e] = s[t][nb][e] * ((e < 2 ? va : vb) * ratio[nb][e & 1]);
+              if (unseen(t, nb, e)) x[e] = 0.f;
+              h[nb][e & 1] = max_nan(h[nb][e & 1], x[e]);
             }
+            w[t][nb] = make_uint2(pack<MT>(x[0], x[1]), pack<MT>(x[2], x[3]));
+          }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) up = up || h[nb][e] > kMost || u[nb][e] < -kLead;
+          for (int e = 0; e < 2; ++e) up = up || !(h[nb][e] <= kMost) || u[nb][e] < -kLead;
         if (__any_sync(~0u, up)) {
+          // Once more, in other units: those of the rows' largest 2^(s - m) scale, whose
+          // exponents go to h.
           float f[NB][2];
+          bool out_of_range = false, moved = false;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float top = over_tokens(h[nb][e]);
-              // Without a unit yet the weights are in units of 2^m.
-              const bool none = u[nb][e] == -INFINITY, to = top > (none ? 0.f : kMost);
-              const float k = to ? lg2(top) : 0.f, low = none ? 0.f : fmaxf(u[nb][e], -kLead);
-              f[nb][e] = none ? 1.f : ex2(u[nb][e] - low - k);
-              if (to || !none) u[nb][e] = low + k;
-              if (to) ratio[nb][e] = ex2(-u[nb][e]);
-              const float by = ex2(-k);
-#pragma unroll
-              for (int t = 0; t < MT16; ++t) s[t][nb][e] *= by, s[t][nb][e + 2] *= by;
+              out_of_range = out_of_range || !(h[nb][e] < 0x1p126f);
+              h[nb][e] = lg2(h[nb][e]) + (u[nb][e] == -INFINITY ? 0.f : fmaxf(u[nb][e], -kLead));
             }
-          rescale(f);
+          if (__any_sync(~0u, out_of_range)) {
+            // Taken without the unit; 2^-9 of it, as s - m <= 8.
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = 0.f;
+#pragma unroll
+                for (int t = 0; t < MT16; ++t) {
+                  const float* by = scales + t * (kScaleBytes / 4);
+                  if (!unseen(t, nb, e)) x = fmaxf(x, s[t][nb][e] * (by[0] * 0x1p-9f));
+                  if (!unseen(t, nb, e + 2)) x = fmaxf(x, s[t][nb][e + 2] * (by[8] * 0x1p-9f));
+                }
+                h[nb][e] = lg2(x) + 9.f;
+              }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // At most 125, where 2^-u and the weights are in range.  -infinity: nothing
+              // but zeros so far, no unit.
+              const float to = fminf(over_tokens(h[nb][e]), 125.f), was = u[nb][e];
+              if (was == -INFINITY || to > was + kSlack) u[nb][e] = to;
+              if (u[nb][e] != -INFINITY) u[nb][e] = fmaxf(u[nb][e], -kLead);
+              f[nb][e] = was == -INFINITY ? 1.f : ex2(was - u[nb][e]);
+              moved = moved || f[nb][e] != 1.f;
+              ratio[nb][e] = u[nb][e] == -INFINITY ? 1.f : ex2(-u[nb][e]);
+            }
+          if (__any_sync(~0u, moved)) rescale(f);
+#pragma unroll
+          for (int t = 0; t < MT16; ++t) {
+            const float va = scales[t * (kScaleBytes / 4)], vb = scales[t * (kScaleBytes / 4) + 8];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              w[t][nb] = make_uint2(pack<MT>(scaled(t, nb, 0, va), scaled(t, nb, 1, va)),
+                                    pack<MT>(scaled(t, nb, 2, vb), scaled(t, nb, 3, vb)));
+          }
         }
       } else if (token + kTokens > len) {
         // Slots behind the last position hold anything: zeros, so that a weight
@@ -818,11 +866,13 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
       // ------------------------------------------------------------ products
 #pragma unroll
       for (int t = 0; t < MT16; ++t) {
-        uint2 w[NB];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          w[nb] = make_uint2(transposed(pack<MT>(s[t][nb][0], s[t][nb][1])),
-                             transposed(pack<MT>(s[t][nb][2], s[t][nb][3])));
+        for (int nb = 0; nb < NB; ++nb) {
+          if (!kEight)
+            w[t][nb] = make_uint2(pack<MT>(s[t][nb][0], s[t][nb][1]),
+                                  pack<MT>(s[t][nb][2], s[t][nb][3]));
+          w[t][nb] = make_uint2(transposed(w[t][nb].x), transposed(w[t][nb].y));
+        }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint4 a, a2;
@@ -839,8 +889,8 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            mma<MT>(o[2 * i][nb], a, w[nb].x, w[nb].y);
-            mma<MT>(o[2 * i + 1][nb], a2, w[nb].x, w[nb].y);
+            mma<MT>(o[2 * i][nb], a, w[t][nb].x, w[t][nb].y);
+            mma<MT>(o[2 * i + 1][nb], a2, w[t][nb].x, w[t][nb].y);
           }
         }
       }

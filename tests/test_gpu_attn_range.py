@@ -35,7 +35,7 @@ def decode_and_check(q, k, v, cache_dtype, scale=1.0, wide=(False, True)):
     """One sequence of n keys k and values v [n][H][D] (fp32) through a cache, q
     [1][T][Hq][D] over it, against 64 bits: bounds of attn_util, where over 8 bits
     the weights' unit is at most the largest exp(s_j) times value scale of a row
-    or, where that is less, 2^-60 exp(m).  Weights below 2^-126 are zero."""
+    or, where that is less, 2^-118 exp(m).  Weights below 2^-126 are zero."""
     n, H, D = k.shape
     T, Hq = q.shape[1:3]
     G = Hq // H
@@ -61,7 +61,7 @@ def decode_and_check(q, k, v, cache_dtype, scale=1.0, wide=(False, True)):
                 seen = torch.arange(n, device="cuda")[None, :] < most[:, None]
                 z = torch.where(seen, rows @ kk.t() * scale, -math.inf)
                 e = torch.exp(z - z.amax(1, keepdim=True))
-                largest = (e * unit).amax(1) + 2.0 ** -60
+                largest = (e * unit).amax(1) + 2.0 ** -118
                 small = (2 * 127 * n * largest)[:, None]
             else:
                 small = ref[3]
@@ -99,3 +99,39 @@ def test_scores_that_rise_far(q_dtype, cache_dtype, D, T, G, n, H, rise, order):
     for spread in (1.0, 400.0):  # value scales near 0.02 and 8
         v = torch.randn((n, H, D), generator=A.gen(8), device="cuda") * spread
         decode_and_check(queries(T, G * H, D, q_dtype), keys_of(size, D, H), v, cache_dtype)
+
+
+@pytest.mark.parametrize("q_dtype", [BF16, F16])
+@pytest.mark.parametrize("D,Hq", [(128, 4), (64, 12), (256, 24)])
+@pytest.mark.parametrize("low", [20, 60, 75, 80, 86, 100, 120])
+@pytest.mark.parametrize("at,H", [(3, 1), (300, 1), (3, 90), (1400, 90)])
+def test_a_value_of_zero_takes_the_softmax(q_dtype, D, Hq, low, at, H):
+    """A key with a value of zero lies `low` nats above all others, which are the
+    whole output; normal keys of its score come after them, or do not."""
+    n = 500 if H == 1 else 2000
+    size = torch.zeros(n, device="cuda")
+    v = torch.randn((n, H, D), generator=A.gen(3), device="cuda")
+    size[at], v[at] = low, 0
+    decode_and_check(queries(1, Hq * H, D, q_dtype), keys_of(size, D, H), v, I8)
+    size[n - 60:n - 20] = low
+    v[n - 60:n - 20] = 50 * 127 * torch.rand(D, generator=A.gen(4), device="cuda")
+    decode_and_check(queries(1, Hq * H, D, q_dtype), keys_of(size, D, H), v, I8)
+    # and those before it far below
+    size[:at] = -2.0 * low
+    decode_and_check(queries(1, Hq * H, D, q_dtype), keys_of(size, D, H), v, I8)
+
+
+@pytest.mark.parametrize("q_dtype", [BF16])
+@pytest.mark.parametrize("exponent", [-136, -130, -126, -100, -40, 40, 100, 117])
+@pytest.mark.parametrize("rise", [0, 50, 200, -50, -200])
+def test_value_scales_at_the_ends_of_fp32(q_dtype, exponent, rise):
+    """Values of this power of two, before and after normal ones; bf16 outputs hold
+    them all."""
+    D = 128
+    for n, H in ((300, 1), (2000, 80)):
+        j = torch.arange(n, device="cuda")
+        v = torch.randn((n, H, D), generator=A.gen(5), device="cuda").clamp(-4, 4)
+        far = v * 2.0 ** exponent
+        half = torch.where(j[:, None, None] < n // 2, far, v)
+        for values in (far, half, half.flip(0)):
+            decode_and_check(queries(1, 4 * H, D, q_dtype), keys_of(j / n * rise, D, H), values, I8)
