@@ -128,11 +128,17 @@ __device__ __forceinline__ float largest(const Eight<__nv_bfloat16>& x) {
   return largest_of_pairs<__nv_bfloat16, __nv_bfloat162>(x);
 }
 
+template <typename XT> __device__ __forceinline__ float clamped(float x) {
+  return sizeof(XT) == 4 ? fminf(fmaxf(x, -127.f), 127.f) : x;
+}
+
 // Eight codes of a unit: q = clamp(rne(x / s)).  The quotient is first taken as
 // t = x * (1 / s), which is within 3e-5 of it (|t| <= 127, three roundings) and
 // so rounds alike unless it lies within 1e-4 of a half: then the warp divides.
-// t + 1.5 * 2^23 rounds t to nearest even and has the code in its low byte; the
-// clamp has nothing to do, |x / s| being at most 127 and a rounding.
+// t + 1.5 * 2^23 rounds t to nearest even and has the code in its low byte.  The
+// clamp has something to do for subnormal s only, by which the warp divides: s is a
+// coarse rounding of max|x| / 127 then, and |x / s| passes 127.5 in fp32 (not in
+// bf16: max|x| >= 2^-133 leaves s 516 steps of 2^-149, and |x / s| below 127.13).
 template <typename XT>
 __device__ __forceinline__ uint2 quantise(const Eight<XT>& x, float s) {
   constexpr float kRound = 12582912.f;
@@ -150,8 +156,8 @@ __device__ __forceinline__ uint2 quantise(const Eight<XT>& x, float s) {
   if (__any_sync(~0u, off > 0.4999f || !(by > 0x1p-120f && by < 0x1p120f))) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      r[e].x = __fdiv_rn(widen(x.x[2 * e]), by) + kRound;
-      r[e].y = __fdiv_rn(widen(x.x[2 * e + 1]), by) + kRound;
+      r[e].x = clamped<XT>(__fdiv_rn(widen(x.x[2 * e]), by)) + kRound;
+      r[e].y = clamped<XT>(__fdiv_rn(widen(x.x[2 * e + 1]), by)) + kRound;
     }
   }
   const auto four = [](float2 a, float2 b) {

@@ -135,3 +135,38 @@ def test_value_scales_at_the_ends_of_fp32(q_dtype, exponent, rise):
         half = torch.where(j[:, None, None] < n // 2, far, v)
         for values in (far, half, half.flip(0)):
             decode_and_check(queries(1, 4 * H, D, q_dtype), keys_of(j / n * rise, D, H), values, I8)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_codes_of_subnormal_scales(dtype, D):
+    """Units whose largest magnitude is a few powers of two above the smallest
+    number: s = max|x| / 127 is rounded coarsely there and |x / s| passes 127."""
+    tops = torch.cat([torch.arange(1, 700), torch.arange(700, 17000, 61),
+                      torch.tensor([16065, 16066, 16128, 16384])]).to(torch.int32)
+    step = 1 if dtype == F32 else 1 << 16  # bf16's smallest number is 2^-133
+    if dtype == BF16:
+        tops = tops[:127]
+    x = (torch.rand((len(tops), 2, D), generator=torch.Generator().manual_seed(D)) * 2 - 1)
+    x = (x * tops[:, None, None]).round().to(torch.int32)
+    x[:, 0, 5], x[:, 1, 7] = tops, -tops
+    x[:, 0, 9], x[:, 1, 11] = -tops, tops
+    bits = x.abs() * step  # the bits of a subnormal number are its multiple of 2^-149
+    bits = torch.where(x < 0, bits - (1 << 31), bits)
+    k = bits.to(torch.int32).view(F32)
+    assert float(k.abs().max()) < 2.0 ** -118
+    if dtype == BF16:
+        assert torch.equal(k.to(BF16).float(), k)
+    top = k.abs().amax(-1)
+    s = torch.from_numpy(top.numpy() / torch.tensor(127.0).numpy())
+    q = torch.from_numpy(k.numpy() / torch.where(s > 0, s, torch.ones(()))[..., None].numpy())
+    assert dtype == BF16 or float(q.abs().max()) > 128
+    q = q.round().clamp(-127, 127).to(I8)
+    pages = -(-len(tops) // 16)
+    cache = pq2.kv_cache(pages, 2, 16, D)
+    pq2.pq2_kv_store(k.to(dtype).cuda(), -k.to(dtype).cuda(), cache, table_of(pages, pages),
+                     ints([len(tops)]))
+    for t, scales, want in ((cache.k, cache.k_scales, q), (cache.v, cache.v_scales, -q)):
+        got = t.transpose(1, 2).reshape(-1, 2, D)[:len(tops)].cpu()
+        assert torch.equal(scales.transpose(1, 2).reshape(-1, 2)[:len(tops)].cpu(), s)
+        assert torch.equal(got, want)
