@@ -185,6 +185,13 @@ __device__ __forceinline__ uint4 ldsm_t(uint32_t addr) {
                : "memory");
   return r;
 }
+// Eight elements with zeros in the place of infinities and NaN.
+template <typename T>
+__device__ __forceinline__ uint4 finite(uint4 x) {
+  constexpr uint32_t kTop = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+  const auto pair = [](uint32_t y) { return y & ~__vcmpeq2(y & kTop, kTop); };
+  return make_uint4(pair(x.x), pair(x.y), pair(x.z), pair(x.w));
+}
 // The transpose of an 8 x 8 matrix of 16-bit elements, a pair of a row a lane.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
@@ -271,42 +278,6 @@ __device__ __forceinline__ void next_tile(Cursor& c, const Params& p) {
   c.next_len = length(p, c.b + 1);
 }
 
-// Four columns of one row by the formula itself, for rows whose sums met an
-// infinity or NaN although they do not see the newest positions: an MMA
-// multiplies every value of a slice by its weight, and 0 * NaN would stay.
-template <typename QT, typename CT, int D>
-__device__ __noinline__ float4 plain_columns(const Params& p, int b, int kh, int R, int d,
-                                             int most, float m, float l) {
-  const QT* q = static_cast<const QT*>(p.a.q) + b * p.a.batch_stride +
-                R / p.group * p.a.token_stride + (kh * p.group + R % p.group) * p.a.head_stride;
-  float o[4] = {};
-#pragma unroll 1
-  for (int j = 0; j < most; ++j) {
-    const int64_t at = j / p.cache.page_size, slot = j - at * p.cache.page_size;
-    const int64_t page =
-        at < p.a.batch.table_width ? __ldg(p.a.batch.table + b * p.a.batch.table_stride + at) : -1;
-    const bool there = page >= 0 && page < p.cache.pages;
-    const int64_t from =
-        page * p.cache.page_stride + kh * p.cache.head_stride + slot * p.cache.token_stride;
-    const int64_t side = (page * p.cache.heads + kh) * p.cache.page_size + slot;
-    float s = 0.f;
-    if (there) {
-      const CT* k = static_cast<const CT*>(p.cache.k) + from;
-#pragma unroll 4
-      for (int i = 0; i < D; ++i) s = fmaf(widen(q[i]), widen(k[i]), s);
-      if (sizeof(CT) == 1) s *= p.cache.k_scales[side];
-    }
-    const float w = ex2(fmaf(s, p.c, -m));
-    if (there) {
-      const CT* v = static_cast<const CT*>(p.cache.v) + from + d;
-      const float vs = sizeof(CT) == 1 ? p.cache.v_scales[side] : 1.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(w, widen(v[i]) * vs, o[i]);
-    }
-  }
-  return make_float4(o[0] / l, o[1] / l, o[2] / l, o[3] / l);
-}
-
 // Four columns of a joined row to out, and its lse: o in units of 2^(m + u), the
 // weights' sum l in units of 2^m.
 template <typename QT, typename CT, int D>
@@ -321,9 +292,6 @@ __device__ __forceinline__ void finish(const Params& p, int b, int kh, int R, in
   } else {
     const float f = (sizeof(CT) == 1 ? ex2(u) : 1.f) / l;
     o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-    const float zero = (o.x + o.y) * 0.f + (o.z + o.w) * 0.f;
-    if (zero != 0.f && l - l == 0.f && most < len)
-      o = plain_columns<QT, CT, D>(p, b, kh, R, d, most, m, l);
   }
   *reinterpret_cast<uint2*>(static_cast<QT*>(p.a.out) + row * D + d) =
       make_uint2(pack<QT>(o.x, o.y), pack<QT>(o.z, o.w));
@@ -851,17 +819,50 @@ __global__ void __launch_bounds__(Geo<CT, D, RT, NB>::threads, 1)
                                     pack<MT>(scaled(t, nb, 2, vb), scaled(t, nb, 3, vb)));
           }
         }
-      } else if (token + kTokens > len) {
-        // Slots behind the last position hold anything: zeros, so that a weight
-        // of zero times them is zero.
-        if (rt == 0) {
-          for (int x = lane; x < G::unit / 16; x += 32)
-            if (x / (G::sixteen / 16) * 16 + (x >> 3) % 16 >= len - token)
-              *reinterpret_cast<uint4*>(ring_p + st * G::unit + x * 16) = make_uint4(0, 0, 0, 0);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      } else if (edge) {
+        // The MMA multiplies every value of the slice by its weight, and 0 * NaN is
+        // not 0.  Slots behind the last position hold anything: zeros.  What is not
+        // finite among the newest positions, which only some rows see, is added to the
+        // sums of those, and then zero too.
+        const int newest = max(len - p.a.T + 1 - token, 0), end = min(len - token, kTokens);
+        constexpr int kPieces = G::rowBytes / 16;
+        uint8_t* unit = ring_p + st * G::unit;
+        const auto at = [&](int j, int piece) {  // 16 bytes of the slice's position j
+          return unit + j / 16 * G::sixteen + piece / 8 * (16 * G::boxBytes) + j % 16 * G::boxBytes +
+                 (piece % 8 ^ j % 8) * 16;
+        };
+        bool odd = false;
+        for (int x = newest * kPieces + lane; x < end * kPieces; x += 32) {
+          const uint4 y = *reinterpret_cast<const uint4*>(at(x / kPieces, x % kPieces)), z = finite<QT>(y);
+          odd = odd || y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w;
         }
-        if (RT > 1) named_bar_sync(1 + slice, RT * 32);
-        __syncwarp();
+        odd = __any_sync(~0u, odd);
+        if (odd) {
+#pragma unroll 1
+          for (int j = newest; j < end; ++j)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              const float y = widen(reinterpret_cast<const QT*>(at(j, i))[g]);
+              if (fabsf(y) < INFINITY) continue;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (token + j < most[nb][e]) o[i / 2][nb][i % 2 * 2 + e] += y;
+            }
+          if (RT > 1) named_bar_sync(1 + slice, RT * 32);
+        }
+        if (odd || token + kTokens > len) {
+          if (rt == 0) {
+            for (int x = (odd ? newest : end) * kPieces + lane; x < kTokens * kPieces; x += 32) {
+              uint4& y = *reinterpret_cast<uint4*>(at(x / kPieces, x % kPieces));
+              y = x < end * kPieces ? finite<QT>(y) : make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          if (RT > 1) named_bar_sync(1 + slice, RT * 32);
+          __syncwarp();
+        }
       }
       // ------------------------------------------------------------ products
 #pragma unroll

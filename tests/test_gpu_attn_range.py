@@ -170,3 +170,68 @@ def test_codes_of_subnormal_scales(dtype, D):
         got = t.transpose(1, 2).reshape(-1, 2, D)[:len(tops)].cpu()
         assert torch.equal(scales.transpose(1, 2).reshape(-1, 2)[:len(tops)].cpu(), s)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,H", [(60, 2), (3000, 2), (900, 60)])
+def test_decode_of_infinities_and_nan_seen_and_not(dtype, D, n, H):
+    """Four new tokens; the newest position's values, which only the last row sees,
+    and some that all rows see are not finite."""
+    T, G = 4, 2
+    g = A.gen(D + n)
+    q = torch.randn((1, T, G * H, D), generator=g, device="cuda").to(dtype)
+    k, v = (torch.randn((n, H, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[5, :, 0] = -8.0 * D ** 0.5  # 64 nats below the others
+    inf = float("inf")
+    v[5, :, 3], v[5, :, 5], v[8, :, 5], v[9, :, 7] = inf, inf, -inf, inf - inf
+    v[n - 1, :, 9], v[n - 1, :, 20:30] = inf - inf, -inf
+    pages = -(-n // 16)
+    cache = pq2.kv_cache(pages, H, 16, D, dtype)
+    pq2.pq2_kv_store(k, v, cache, table_of(pages, pages), ints([n]))
+    lse = torch.empty(q.shape[:-1], device="cuda")
+    out = pq2.pq2_attn_decode(q, cache, table_of(pages, pages), ints([n]), lse=lse)
+    odd = [3, 5, 7, 9, *range(20, 30)]
+    clean = torch.where(v.isfinite(), v, 0).double()
+    most = n - T + 1 + torch.arange(T, device="cuda").repeat_interleave(G)
+    for h in sorted({0, H // 2, H - 1}):
+        at = slice(h * G, h * G + G)
+        ref = A.attend(q[0, :, at].double().reshape(T * G, D), k[:, h].double(), clean[:, h], most,
+                       D ** -0.5)
+        o, z = out[0, :, at].reshape(T * G, D), lse[0, :, at].reshape(T * G)
+        A.check_rows(o[:, 30:], z, (ref[0][:, 30:], ref[1], *(x[:, 30:] for x in ref[2:4]), *ref[4:]),
+                     D, dtype)
+        before = o[:G * (T - 1)]
+        A.check_rows(before[:, [9, *range(20, 30)]], None,
+                     tuple(x[:G * (T - 1), [9, *range(20, 30)]] if x.dim() == 2
+                           else x[:G * (T - 1)] for x in ref), D, dtype)
+        assert not bool(before[:, 3].isfinite().any()) and bool(o[:, [5, 7]].isnan().all())
+        assert not bool(o[G * (T - 1):, odd].isfinite().any())
+
+
+def test_a_nan_costs_little_in_the_decode():
+    """Values of the first or of the newest position that are NaN, two new tokens:
+    no more than 5 times the time without."""
+    n, H = 60000, 8
+    cache = pq2.kv_cache(n // 16, H, 16, 128, BF16)
+    for t in cache[:2]:
+        t.normal_(generator=A.gen(1))
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda")[None]
+    q = torch.randn((1, 2, H, 128), generator=A.gen(2), device="cuda").bfloat16()
+    lens, out, took = ints([n]), torch.empty_like(q), []
+    for bad in (None, (n // 16 - 1, 15), (0, 0)):
+        if bad:
+            cache.v[bad[0], :, bad[1]] = float("nan")
+        best = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            pq2.pq2_attn_decode(q, cache, table, lens, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        took.append(min(best))
+        assert bool(out[:, 0].isnan().all()) == (bad == (0, 0))
+        assert bool(out[:, 1].isnan().all()) == (bad is not None)
+    assert max(took[1:]) <= 5 * took[0], took
