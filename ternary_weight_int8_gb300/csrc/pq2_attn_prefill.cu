@@ -166,30 +166,94 @@ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major, bool negate_a) 
          (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
 }
 
-// 32 columns of one row by the formula itself, for rows whose sums met an
-// infinity or NaN: the MMA multiplies every value of a key tile by its weight,
-// and 0 * NaN of a key that the row does not see would stay in the row.
+// The columns of one row that are not finite once more, by the formula itself and
+// by a whole warp: the MMA multiplies every value of a key tile by its weight, and
+// 0 * NaN of a key that the row does not see would stay in the row.  A column with
+// infinities or NaN among the values that the row does see is their sum (a weight
+// that rounds to zero is not one), and needs no scores.
 template <typename T, int D>
-__device__ __noinline__ void plain_columns(const T* q, const T* k, int64_t k_token, const T* v,
-                                           int64_t v_token, int most, float c, float mc,
-                                           float factor, T* out) {
-#pragma unroll 1
-  for (int d0 = 0; d0 < 32; d0 += 8) {
-    float o[8] = {};
-#pragma unroll 1
-    for (int j = 0; j < most; ++j) {
-      float s = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < D; ++d) s = fmaf(widen(q[d]), widen(k[(int64_t)j * k_token + d]), s);
-      const float p = ex2(fmaf(s, c, -mc));
+__device__ __noinline__ void plain_row(const T* q, const T* k, int64_t k_token, const T* v,
+                                       int64_t v_token, int most, float c, bool negative, T* out) {
+  constexpr int E = D / 32;  // columns of a lane
+  struct alignas(2 * E) Columns { T x[E]; };
+  const int lane = threadIdx.x & 31;
+  out += lane * E, v += lane * E;
+  bool bad[E], none = true;
+  float odd[E], sum[E];  // of what is not finite, of weights times values
 #pragma unroll
-      for (int d = 0; d < 8; ++d) o[d] = fmaf(p, widen(v[(int64_t)j * v_token + d0 + d]), o[d]);
-    }
-    uint4 w;
-    w.x = pack<T>(o[0] * factor, o[1] * factor), w.y = pack<T>(o[2] * factor, o[3] * factor);
-    w.z = pack<T>(o[4] * factor, o[5] * factor), w.w = pack<T>(o[6] * factor, o[7] * factor);
-    *reinterpret_cast<uint4*>(out + d0) = w;
+  for (int e = 0; e < E; ++e) {
+    bad[e] = !(fabsf(widen(out[e])) < INFINITY);
+    none = none && !bad[e];
+    odd[e] = sum[e] = 0.f;
   }
+  if (__all_sync(~0u, none)) return;
+#pragma unroll 1
+  for (int j0 = 0; j0 < most; j0 += 16) {
+    Columns y[16];  // behind the last key its values once more, which change nothing
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      y[j] = *reinterpret_cast<const Columns*>(v + (int64_t)min(j0 + j, most - 1) * v_token);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (!(fabsf(widen(y[j].x[e])) < INFINITY)) odd[e] += widen(y[j].x[e]);
+    bool settled = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) settled = settled && (!bad[e] || odd[e] != odd[e]);
+    if (__all_sync(~0u, settled)) break;
+  }
+  bool settled = true;
+#pragma unroll
+  for (int e = 0; e < E; ++e) settled = settled && (!bad[e] || odd[e] != 0.f);
+  float m = -INFINITY, l = 0.f;
+  if (!__all_sync(~0u, settled)) {
+    // A key a lane for the scores, then a key at a time for the values.
+#pragma unroll 1
+    for (int j0 = 0; j0 < most; j0 += 32) {
+      float s = -INFINITY;
+      if (j0 + lane < most) {
+        const T* key = k + (int64_t)(j0 + lane) * k_token;
+        s = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 8) {
+          const uint4 a = *reinterpret_cast<const uint4*>(q + d);
+          const uint4 b = *reinterpret_cast<const uint4*>(key + d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            s = fmaf(widen(reinterpret_cast<const T*>(&a)[e]),
+                     widen(reinterpret_cast<const T*>(&b)[e]), s);
+        }
+        if (negative) s = -s;
+      }
+      float top = s;
+#pragma unroll
+      for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      top = fmaxf(top, m);
+      const float f = m == -INFINITY ? 0.f : ex2((m - top) * c);
+      const float w = s == -INFINITY ? 0.f : ex2((s - top) * c);
+      float more = w;
+#pragma unroll
+      for (int o = 16; o; o /= 2) more += __shfl_xor_sync(~0u, more, o);
+      l = fmaf(l, f, more), m = top;
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] *= f;
+#pragma unroll 8
+      for (int j = 0; j < 32; ++j) {
+        const float by = __shfl_sync(~0u, w, j);
+        if (j0 + j >= most) continue;
+        const Columns y = *reinterpret_cast<const Columns*>(v + (int64_t)(j0 + j) * v_token);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] = fmaf(by, widen(y.x[e]), sum[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (bad[e]) {
+      const uint32_t y = pack<T>(odd[e] != 0.f ? odd[e] : sum[e] / l, 0.f);
+      out[e] = *reinterpret_cast<const T*>(&y);
+    }
 }
 
 template <typename T, int D>
@@ -602,7 +666,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
         __syncwarp();
       }
     } else {
-    uint32_t bad = 0;  // groups of 32 columns that are not finite
+    bool bad = false;  // something is not finite
 #pragma unroll 1
     for (int d = 0; d < D; d += 32) {
       float o[32];
@@ -616,7 +680,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
         if (most <= 0) o[i] = 0.f;
         zero = fmaf(o[i], 0.f, zero);
       }
-      if (zero != 0.f) bad |= 1u << d / 32;
+      bad = bad || zero != 0.f;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         uint4 w;
@@ -636,14 +700,17 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     }
     __syncwarp();
     if (live && p.lse) p.lse[row] = most > 0 ? mc * kLn2 + logf(l) : -INFINITY;
-    if (live && bad && factor - factor == 0.f) {
-      const T* q = static_cast<const T*>(p.q) + ((int64_t)q0 + t) * p.q_token + h * p.q_head;
-      const T* k = static_cast<const T*>(p.k) + (int64_t)k0 * p.k_token + head * p.k_head;
-      const T* v = static_cast<const T*>(p.v) + (int64_t)k0 * p.v_token + head * p.v_head;
-      for (int d = 0; d < D; d += 32)
-        if (bad >> d / 32 & 1)
-          plain_columns<T, D>(q, k, p.k_token, v + d, p.v_token, most, p.negative ? -p.c : p.c, mc,
-                              factor, static_cast<T*>(p.out) + row * D + d);
+    uint32_t again = __ballot_sync(~0u, live && bad && factor - factor == 0.f);
+    while (again) {
+      const int of = __ffs(again) - 1;
+      again &= again - 1;
+      const int token = __shfl_sync(~0u, t, of), qh = __shfl_sync(~0u, h, of);
+      plain_row<T, D>(
+          static_cast<const T*>(p.q) + ((int64_t)q0 + token) * p.q_token + qh * p.q_head,
+          static_cast<const T*>(p.k) + (int64_t)k0 * p.k_token + head * p.k_head, p.k_token,
+          static_cast<const T*>(p.v) + (int64_t)k0 * p.v_token + head * p.v_head, p.v_token,
+          __shfl_sync(~0u, most, of), p.c, p.negative,
+          static_cast<T*>(p.out) + __shfl_sync(~0u, row, of) * D);
     }
     }
   }
@@ -716,12 +783,12 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const Params p) {
         most > 0 ? pack<T>(sum[e] * factor, sum[e + 1] * factor) : 0u;
   if (lane == 0 && p.lse) p.lse[row] = most > 0 ? m * kLn2 + logf(l) : -INFINITY;
   __syncwarp();
-  if (odd && most > 0 && factor - factor == 0.f && lane < E) {
-    const int kh = h / p.group, d = lane * 32;
-    plain_columns<T, D>(static_cast<const T*>(p.q) + i * p.q_token + h * p.q_head,
-                        static_cast<const T*>(p.k) + k0 * p.k_token + kh * p.k_head, p.k_token,
-                        static_cast<const T*>(p.v) + k0 * p.v_token + kh * p.v_head + d, p.v_token,
-                        most, p.negative ? -p.c : p.c, m, factor, out + d);
+  if (odd && most > 0 && factor - factor == 0.f) {
+    const int kh = h / p.group;
+    plain_row<T, D>(static_cast<const T*>(p.q) + i * p.q_token + h * p.q_head,
+                    static_cast<const T*>(p.k) + k0 * p.k_token + kh * p.k_head, p.k_token,
+                    static_cast<const T*>(p.v) + k0 * p.v_token + kh * p.v_head, p.v_token, most,
+                    p.c, p.negative, out);
   }
 }
 

@@ -172,6 +172,76 @@ def test_codes_of_subnormal_scales(dtype, D):
         assert torch.equal(got, want)
 
 
+def sums(x):
+    return torch.tensor([0, *x], dtype=torch.int32, device="cuda").cumsum(0).int()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq,nk", [(300, 300), (60, 9000)])
+def test_infinities_and_nan_seen_and_not(dtype, D, nq, nk):
+    """Columns with an infinity, with both, with NaN, and with one that only later
+    rows see; the key of the first has no weight that 16 bits could hold."""
+    g = A.gen(D + nq)
+    q = torch.randn((nq, 4, D), generator=g, device="cuda").to(dtype)
+    k = torch.randn((nk, 2, D), generator=g, device="cuda").to(dtype)
+    v = torch.randn((nk, 2, D), generator=g, device="cuda").to(dtype)
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[5, :, 0] = -8.0 * D ** 0.5  # 64 nats below the others
+    late = nk - nq + 40
+    clean = v.clone()
+    clean[:, :, [3, 5, 7, 9]] = 0
+    v[5, :, 3], v[5, :, 5], v[8, :, 5] = float("inf"), float("inf"), -float("inf")
+    v[9, :, 7], v[late, :, 9] = float("nan"), -float("inf")
+    cu_q, cu_k = sums([nq]), sums([nk])
+    t = torch.arange(nq, device="cuda")
+    for causal in (True, False):
+        out = pq2.pq2_attn_prefill(q, k, v, cu_q, cu_k, causal=causal)
+        most = nk - nq + 1 + t if causal else torch.full((nq,), nk, device="cuda")
+        inf = float("inf")
+        for h in range(4):
+            seen = clean[:, h // 2].double()
+            seen[:, [3, 5, 7, 9]] = torch.where(torch.isfinite(v[:, h // 2, [3, 5, 7, 9]]),
+                                                v[:, h // 2, [3, 5, 7, 9]], 0.0).double()
+            ref = A.attend(q[:, h].double(), k[:, h // 2].double(), seen, most, D ** -0.5)
+            # rows that do not see what is not finite, and all other columns
+            fine = torch.ones((nq, D), dtype=torch.bool, device="cuda")
+            fine[:, 3], fine[:, 5], fine[:, 7] = most <= 5, most <= 5, most <= 9
+            fine[:, 9] = most <= late
+            got = torch.where(fine, out[:, h], torch.zeros_like(out[:, h]))
+            want = (torch.where(fine, ref[0], 0.0), ref[1],
+                    *(torch.where(fine, x, 0.0) for x in ref[2:4]), *ref[4:])
+            A.check_rows(got, None, want, D, dtype)
+            assert bool((out[most > 5, h, 3] == inf).all())
+            assert bool((out[(most > 5) & (most <= 8), h, 5] == inf).all())
+            assert bool(out[most > 8, h, 5].isnan().all())
+            assert bool(out[most > 9, h, 7].isnan().all())
+            assert bool((out[most > late, h, 9] == -inf).all())
+
+
+def test_a_nan_costs_little():
+    """A prompt whose first values are NaN takes no more than 30 times its time
+    without (each row looks for what it sees, which ends with the first)."""
+    n = 4096
+    q = torch.randn((n, 8, 128), generator=A.gen(1), device="cuda").bfloat16()
+    k, v = (torch.randn((n, 2, 128), generator=A.gen(s), device="cuda").bfloat16() for s in (2, 3))
+    bad, out, cu = v.clone(), torch.empty_like(q), sums([n])
+    bad[0] = float("nan")
+    took = []
+    for values in (v, bad, v, bad):
+        best = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            pq2.pq2_attn_prefill(q, k, values, cu, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        took.append(min(best))
+    assert bool(out.isnan().all())
+    assert took[3] <= 30 * took[2], took
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n,H", [(60, 2), (3000, 2), (900, 60)])
