@@ -43,6 +43,10 @@ namespace {
 constexpr int BM = 128, BN = 128;  // rows of a query tile, keys of a key tile
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;  // how far m may stay behind, in powers of two
+// Weights are 2^(c s - fl(c m)), one multiply-add a score: they and their sums are in
+// units of 2^fl(c m).  From this |c m| on the rounding may carry them out of range
+// (fp16's at 2^27, fp32's at 2^32); such rows are computed again, c (s - m) a weight.
+constexpr float kFar = 16777216.f;
 
 template <int D>
 struct Geo {
@@ -76,7 +80,7 @@ struct Params {
   int causal;
   int splits;     // of a tile's keys; with more than one:
   float* parts;   // [splits][q_rows][q_heads][dim], sums of weights times values
-  float2* stats;  // [splits][q_rows][q_heads], maximum (powers of two) and sum of weights
+  float2* stats;  // [splits][q_rows][q_heads], maximum (powers of two; infinity: far) and sum of weights
 };
 
 // Shared-memory matrix descriptor of a 128-byte swizzled operand whose M or N
@@ -170,10 +174,12 @@ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major, bool negate_a) 
 // by a whole warp: the MMA multiplies every value of a key tile by its weight, and
 // 0 * NaN of a key that the row does not see would stay in the row.  A column with
 // infinities or NaN among the values that the row does see is their sum (a weight
-// that rounds to zero is not one), and needs no scores.
+// that rounds to zero is not one), and needs no scores.  all: every column and the
+// row's lse.
 template <typename T, int D>
 __device__ __noinline__ void plain_row(const T* q, const T* k, int64_t k_token, const T* v,
-                                       int64_t v_token, int most, float c, bool negative, T* out) {
+                                       int64_t v_token, int most, float c, bool negative, T* out,
+                                       bool all, float* lse) {
   constexpr int E = D / 32;  // columns of a lane
   struct alignas(2 * E) Columns { T x[E]; };
   const int lane = threadIdx.x & 31;
@@ -182,7 +188,7 @@ __device__ __noinline__ void plain_row(const T* q, const T* k, int64_t k_token, 
   float odd[E], sum[E];  // of what is not finite, of weights times values
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    bad[e] = !(fabsf(widen(out[e])) < INFINITY);
+    bad[e] = all || !(fabsf(widen(out[e])) < INFINITY);
     none = none && !bad[e];
     odd[e] = sum[e] = 0.f;
   }
@@ -203,7 +209,7 @@ __device__ __noinline__ void plain_row(const T* q, const T* k, int64_t k_token, 
     for (int e = 0; e < E; ++e) settled = settled && (!bad[e] || odd[e] != odd[e]);
     if (__all_sync(~0u, settled)) break;
   }
-  bool settled = true;
+  bool settled = !all;
 #pragma unroll
   for (int e = 0; e < E; ++e) settled = settled && (!bad[e] || odd[e] != 0.f);
   float m = -INFINITY, l = 0.f;
@@ -254,6 +260,7 @@ __device__ __noinline__ void plain_row(const T* q, const T* k, int64_t k_token, 
       const uint32_t y = pack<T>(odd[e] != 0.f ? odd[e] : sum[e] / l, 0.f);
       out[e] = *reinterpret_cast<const T*>(&y);
     }
+  if (all && lse && lane == 0) *lse = m * c * kLn2 + logf(l);
 }
 
 template <typename T, int D>
@@ -539,6 +546,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t o_tmem = tmem + lanes + G::oCol + s * D;
     float m = -INFINITY, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+    bool far = false;
     for (int j = 0; j < tiles; ++j) {
       const int slot = kTiles == 2 ? s : j & 1;
       const uint32_t s_tmem = tmem + lanes + slot * BN;
@@ -563,11 +571,12 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
       const float high = max3(top[0], top[1], fmaxf(top[2], top[3]));
       if (j == 0) {
         m = high;
+        far = fabsf(m * p.c) > kFar && m != -INFINITY;
       } else {
         const bool rise = (high - m) * p.c > kSlack;
         if (__any_sync(~0u, rise)) {
-          const float f = rise ? ex2((m - high) * p.c) : 1.f;
-          if (rise) m = high;
+          const float to = __fmul_rn(high, p.c), f = rise ? ex2(__fmul_rn(m, p.c) - to) : 1.f;
+          if (rise) m = high, far = far || fabsf(to) > kFar;
           l0 *= f, l1 *= f, l2 *= f, l3 *= f;
           ok = ok && mbar_wait(&o_full[s], (j - 1) & 1);
           tc_fence_after();
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     if (p.splits > 1) {
       // Two rounds of half the columns, in 32 bits.
       const int64_t part = (int64_t)blockIdx.y * p.q_rows * p.q_heads;
-      if (live) p.stats[part + row] = make_float2(m == -INFINITY ? m : mc, l);
+      if (live) p.stats[part + row] = make_float2(far ? INFINITY : m == -INFINITY ? m : mc, l);
 #pragma unroll 1
       for (int round = 0; round < 2; ++round) {
 #pragma unroll 1
@@ -700,17 +709,18 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1)
     }
     __syncwarp();
     if (live && p.lse) p.lse[row] = most > 0 ? mc * kLn2 + logf(l) : -INFINITY;
-    uint32_t again = __ballot_sync(~0u, live && bad && factor - factor == 0.f);
+    uint32_t again = __ballot_sync(~0u, live && (far || (bad && factor - factor == 0.f)));
     while (again) {
       const int of = __ffs(again) - 1;
       again &= again - 1;
       const int token = __shfl_sync(~0u, t, of), qh = __shfl_sync(~0u, h, of);
+      const int64_t to = __shfl_sync(~0u, row, of);
       plain_row<T, D>(
           static_cast<const T*>(p.q) + ((int64_t)q0 + token) * p.q_token + qh * p.q_head,
           static_cast<const T*>(p.k) + (int64_t)k0 * p.k_token + head * p.k_head, p.k_token,
           static_cast<const T*>(p.v) + (int64_t)k0 * p.v_token + head * p.v_head, p.v_token,
-          __shfl_sync(~0u, most, of), p.c, p.negative,
-          static_cast<T*>(p.out) + __shfl_sync(~0u, row, of) * D);
+          __shfl_sync(~0u, most, of), p.c, p.negative, static_cast<T*>(p.out) + to * D,
+          __shfl_sync(~0u, far, of), p.lse ? p.lse + to : nullptr);
     }
     }
   }
@@ -762,7 +772,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const Params p) {
   T* out = static_cast<T*>(p.out) + row * D;
   // Rows with sums that are not finite, or that see nothing: which keys do they
   // see?
-  const bool odd = __any_sync(~0u, zero != 0.f) || l == 0.f;
+  const bool far = __any_sync(~0u, ml.x == INFINITY);
+  const bool odd = far || __any_sync(~0u, zero != 0.f) || l == 0.f;
   int most = 1, k0 = 0;
   if (odd) {
     int lo = 0, hi = p.B + 1;
@@ -783,12 +794,12 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const Params p) {
         most > 0 ? pack<T>(sum[e] * factor, sum[e + 1] * factor) : 0u;
   if (lane == 0 && p.lse) p.lse[row] = most > 0 ? m * kLn2 + logf(l) : -INFINITY;
   __syncwarp();
-  if (odd && most > 0 && factor - factor == 0.f) {
+  if (odd && most > 0 && (far || factor - factor == 0.f)) {
     const int kh = h / p.group;
     plain_row<T, D>(static_cast<const T*>(p.q) + i * p.q_token + h * p.q_head,
                     static_cast<const T*>(p.k) + k0 * p.k_token + kh * p.k_head, p.k_token,
                     static_cast<const T*>(p.v) + k0 * p.v_token + kh * p.v_head, p.v_token, most,
-                    p.c, p.negative, out);
+                    p.c, p.negative, out, far, p.lse ? p.lse + row : nullptr);
   }
 }
 

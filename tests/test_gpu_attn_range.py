@@ -305,3 +305,72 @@ def test_a_nan_costs_little_in_the_decode():
         assert bool(out[:, 0].isnan().all()) == (bad == (0, 0))
         assert bool(out[:, 1].isnan().all()) == (bad is not None)
     assert max(took[1:]) <= 5 * took[0], took
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_prefill_of_scores_in_the_billions(dtype, D, sign):
+    """Scales to 1e6 of products from one to some thousands, each exact: a
+    sequence of one key gives its value, two of unequal scores the larger one's,
+    two of equal scores their mean."""
+    products = torch.cat([torch.arange(1, 400), torch.arange(400, 6000, 37)]).tolist()
+    n = len(products)
+    q = torch.zeros((n, 2, D), dtype=dtype, device="cuda")
+    k = torch.zeros((n, 1, D), dtype=dtype, device="cuda")
+    # a * 64 + b, both exact in 8 bits
+    p = torch.tensor(products, device="cuda")
+    q[:, :, 0], q[:, :, 1] = 64.0, 1.0
+    k[:, 0, 0], k[:, 0, 1] = (p // 64).to(dtype), (p % 64).to(dtype)
+    k *= sign
+    v = torch.randn((n, 1, D), generator=A.gen(2), device="cuda").to(dtype)
+    lse = torch.empty((n, 2), device="cuda")
+    out = pq2.pq2_attn_prefill(q, k, v, sums([1] * n), scale=1e6 * sign, lse=lse)
+    tol = torch.finfo(dtype).eps * v.float().abs() + 2.0 ** -20
+    assert bool(((out.float() - v.float()).abs() <= tol).all())
+    want = p.double()[:, None] * 1e6
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -21 * want).all())
+    # pairs: (products[0], [1]), ...; rows see both, or the first alone
+    pairs = sums([2] * (n // 2))
+    for causal in (True, False):
+        out = pq2.pq2_attn_prefill(q, k, v, pairs, scale=1e6 * sign, causal=causal)
+        for i in range(2):
+            mine = v[1:n // 2 * 2:2] if i or not causal else v[0:n // 2 * 2:2]
+            tol = torch.finfo(dtype).eps * mine.float().abs() + 2.0 ** -20
+            assert bool(((out[i:n // 2 * 2:2].float() - mine.float()).abs() <= tol).all())
+    k[1::2] = k[0:n // 2 * 2:2]
+    out = pq2.pq2_attn_prefill(q, k, v, pairs, scale=1e6 * sign, causal=False)
+    a, b = v[0:n // 2 * 2:2].float(), v[1:n // 2 * 2:2].float()
+    tol = torch.finfo(dtype).eps * (a.abs() + b.abs()) + 2.0 ** -20
+    for i in range(2):
+        assert bool(((out[i:n // 2 * 2:2].float() - (a + b) / 2).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("nq,nk", [(40, 9000), (300, 300), (700, 700)])
+@pytest.mark.parametrize("order", ["rising", "falling", "steps"])
+def test_prefill_of_many_keys_in_the_billions(dtype, D, nq, nk, order):
+    """Maxima in the billions that rise or fall over the tiles and the parts: every
+    row's output is the mean of the values of its largest scores."""
+    j = torch.arange(nk, device="cuda")
+    p = {"rising": 500 + j // 5, "falling": 2500 - j // 5, "steps": 1000 + (j // 190) * 3}[order]
+    p = p.clamp(max=8000)
+    q = torch.zeros((nq, 2, D), dtype=dtype, device="cuda")
+    k = torch.zeros((nk, 1, D), dtype=dtype, device="cuda")
+    q[:, :, 0], q[:, :, 1] = 64.0, 1.0
+    k[:, 0, 0], k[:, 0, 1] = (p // 64).to(dtype), (p % 64).to(dtype)
+    v = torch.randn((nk, 1, D), generator=A.gen(2), device="cuda").to(dtype)
+    assert nk < 9000 or pq2.lib().pq2_attn_prefill_workspace_bytes(1, nq, nk, 2, 1, D)
+    for causal in (True, False):
+        out = pq2.pq2_attn_prefill(q, k, v, sums([nq]), sums([nk]), scale=1e6, causal=causal)
+        most = nk - nq + 1 + torch.arange(nq, device="cuda") if causal else \
+            torch.full((nq,), nk, device="cuda")
+        seen = j[None, :] < most[:, None]
+        top = torch.where(seen, p[None, :], -1).amax(1)
+        w = (seen & (p[None, :] == top[:, None])).double()
+        w /= w.sum(1, keepdim=True)
+        want, size = w @ v[:, 0].double(), w @ v[:, 0].double().abs()
+        # equal weights are powers of two of each other exactly; sums and out's rounding
+        tol = torch.finfo(dtype).eps * size + 2.0 ** -18 * size.amax()
+        assert bool(((out.double() - want[:, None]).abs() <= tol[:, None]).all())
