@@ -9,6 +9,11 @@ Two levels:
   * ``pq2_prepare``, ``pq2_quantize_act``, ``pq2_mmv``, ``pq2_mm``,
     ``pq2_debug_group_dots`` — the same names taking torch tensors, allocating
     outputs with torch when not given, and passing the current torch stream.
+
+A call with ``stream`` runs on that stream, and what the cache's and the
+attention's calls allocate belongs to it: a result is used on another stream
+after that one has waited for it, as with any torch stream, and let go of when
+that use is done (or after ``record_stream``).
 """
 from __future__ import annotations
 
@@ -158,6 +163,16 @@ def _stream(stream):
     if _raw_stream is None or _device is None:
         return torch.cuda.current_stream().cuda_stream
     return _raw_stream(_device())
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor that belongs to the call's stream: torch gives a block that the
+    current stream has let go of to its next tensor at once, while kernels queued
+    there may still use it, which another stream does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 _DT = {torch.bfloat16: PQ2_BF16, torch.float16: PQ2_F16, torch.float32: PQ2_F32}
@@ -793,8 +808,7 @@ def pq2_kv_load(cache: KVCache, table, lens, cu=None, tokens=None, out=None,
     if out is None:
         if tokens is None:
             raise ValueError("either out or tokens must be given")
-        out = [torch.empty((tokens, heads, dim), dtype=out_dtype, device=cache.k.device)
-               for _ in range(2)]
+        out = [_new((tokens, heads, dim), out_dtype, cache.k.device, stream) for _ in range(2)]
     k, v = out
     shape = (k.shape[0] if tokens is None else tokens, heads, dim)
     dtype = _dtype_of(k)
@@ -811,10 +825,7 @@ _attn_bytes = {}
 
 
 def _workspace(nbytes, like, stream):
-    w = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None and w.is_cuda:
-        w.record_stream(stream)  # it is let go of before the work on that stream is done
-    return w
+    return _new(nbytes, torch.uint8, like.device, stream)
 
 
 _kept = threading.local()  # .by: {(device, stream): a workspace of this thread's calls on it}
@@ -836,11 +847,11 @@ def _kept_workspace(nbytes, like, stream):
     return w
 
 
-def _attn_outputs(q, out, lse):
+def _attn_outputs(q, out, lse, stream):
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"Expected a bfloat16 or float16 tensor, not {q.dtype}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new(q.shape, q.dtype, q.device, stream)
     else:
         _check_out(out, q.shape, q.dtype)
     if lse is not None:
@@ -866,7 +877,7 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
     B, stride, width = _check_table(table, lens)
     if shape[0] != B:
         raise ValueError("q must have a row per row of the table")
-    out = _attn_outputs(q, out, lse)
+    out = _attn_outputs(q, out, lse, stream)
     T, T_stride = (1, 0) if len(shape) == 3 else (shape[1], st[1])
     if cache.k.dtype not in (q.dtype, torch.int8):
         raise ValueError("the cache must have q's type, or int8")
@@ -907,7 +918,7 @@ def pq2_attn_prefill(q, k, v, cu_q, cu_k=None, scale=None, causal: bool = True, 
     cu_k = cu_q if cu_k is None else cu_k
     _check_ints(cu_q, "cu_q")
     _check_ints(cu_k, "cu_k", cu_q.shape[0])
-    out = _attn_outputs(q, out, lse)
+    out = _attn_outputs(q, out, lse, stream)
     rows, heads, dim = q_shape
     keys, kv_heads, B = k_shape[0], k_shape[1], cu_q.shape[0] - 1
     if 1 in q_shape or 1 in k_shape:
