@@ -10,10 +10,10 @@ Two levels:
     ``pq2_debug_group_dots`` — the same names taking torch tensors, allocating
     outputs with torch when not given, and passing the current torch stream.
 
-A call with ``stream`` runs on that stream, and what the cache's and the
-attention's calls allocate belongs to it: a result is used on another stream
-after that one has waited for it, as with any torch stream, and let go of when
-that use is done (or after ``record_stream``).
+A call with ``stream`` runs on that stream, and what it allocates belongs to
+it: a result is used on another stream after that one has waited for it, as with
+any torch stream, and let go of when that use is done (or after
+``record_stream``).
 """
 from __future__ import annotations
 
@@ -188,9 +188,9 @@ def pq2_prepare(raw: torch.Tensor, K: int, codes=None, scales=None, stream=None)
     if raw.dtype != torch.uint8 or raw.dim() != 2 or raw.stride(1) != 1:
         raise ValueError("raw must be a 2-D uint8 tensor with unit column stride")
     if codes is None:
-        codes = torch.empty((N, K // 4), dtype=torch.uint8, device=raw.device)
+        codes = _new((N, K // 4), torch.uint8, raw.device, stream)
     if scales is None:
-        scales = torch.empty((N, K // GROUP), dtype=torch.float16, device=raw.device)
+        scales = _new((N, K // GROUP), torch.float16, raw.device, stream)
     _check("pq2_prepare", lib().pq2_prepare(_ptr(raw), raw.stride(0), N, K, _ptr(codes),
                                             _ptr(scales), _stream(stream)))
     return codes, scales
@@ -203,11 +203,11 @@ def pq2_quantize_act(x: torch.Tensor, layout: int = PQ2_Q_PLANES, q=None, sx=Non
         raise ValueError("x must be 2-D with unit column stride")
     M, K = x.shape
     if q is None:
-        q = q_buffer(M, K, layout, x.device)
+        q = q_buffer(M, K, layout, x.device, stream)
     if sx is None:
-        sx = torch.empty((M, K // GROUP), dtype=torch.float32, device=x.device)
+        sx = _new((M, K // GROUP), torch.float32, x.device, stream)
     if qsum is None and want_qsum:
-        qsum = torch.empty((M, K // GROUP), dtype=torch.int32, device=x.device)
+        qsum = _new((M, K // GROUP), torch.int32, x.device, stream)
     _check("pq2_quantize_act",
            lib().pq2_quantize_act(_ptr(x), _DT[x.dtype], x.stride(0), M, K, _ptr(q), layout,
                                   _ptr(sx), _ptr(qsum), _stream(stream)))
@@ -220,7 +220,7 @@ def pq2_mmv(q_planes, sx, qsum, codes, scales, y=None, out_dtype=torch.float32,
     M, K = q_planes.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_planes.device)
+        y = _new((M, N), out_dtype, q_planes.device, stream)
     yd = _DT[y.dtype]
     args = (_ptr(q_planes), _ptr(sx), _ptr(qsum), _ptr(codes), _ptr(scales), _ptr(y), yd, M,
             N, K)
@@ -240,7 +240,7 @@ def pq2_mmv_tc(q_mmv16, sx, qcorr, codes, scales, y=None, out_dtype=torch.float3
     M, K = q_mmv16.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_mmv16.device)
+        y = _new((M, N), out_dtype, q_mmv16.device, stream)
     _check("pq2_mmv_tc", lib().pq2_mmv_tc(_ptr(q_mmv16), _ptr(sx), _ptr(qcorr), _ptr(codes),
                                           _ptr(scales), _ptr(y), _DT[y.dtype], M, N, K, flags,
                                           _ptr(status), _stream(stream)))
@@ -260,10 +260,10 @@ def pq2_linear(x, codes, scales, y=None, out_dtype=torch.float32, workspace=None
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     wb = linear_workspace_bytes(M, K)
     if workspace is None:
-        workspace = torch.empty(wb, dtype=torch.uint8, device=x.device)
+        workspace = _new(wb, torch.uint8, x.device, stream)
     _check("pq2_linear", lib().pq2_linear(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, _ptr(codes), _ptr(scales), _ptr(y),
         _DT[y.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -277,9 +277,9 @@ def pq2_quantize_act_grouped(x: torch.Tensor, act_group: int, layout: int = PQ2_
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit column stride")
     M, K = x.shape
-    q = q_buffer(M, K, layout, x.device)
-    sx = torch.empty((M, K // act_group), dtype=torch.float32, device=x.device)
-    qsum = torch.empty((M, K // act_group), dtype=torch.int32, device=x.device)
+    q = q_buffer(M, K, layout, x.device, stream)
+    sx = _new((M, K // act_group), torch.float32, x.device, stream)
+    qsum = _new((M, K // act_group), torch.int32, x.device, stream)
     _check("pq2_quantize_act_grouped", lib().pq2_quantize_act_grouped(
         _ptr(x), _DT[x.dtype], x.stride(0), M, K, act_group, _ptr(q), layout, _ptr(sx),
         _ptr(qsum), _stream(stream)))
@@ -292,7 +292,7 @@ def pq2_mmv_grouped(q_planes, sx, qsum, codes, scales, act_group: int, y=None,
     M, K = q_planes.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_planes.device)
+        y = _new((M, N), out_dtype, q_planes.device, stream)
     _check("pq2_mmv_grouped", lib().pq2_mmv_grouped(
         _ptr(q_planes), _ptr(sx), _ptr(qsum), _ptr(codes), _ptr(scales), _ptr(y), _DT[y.dtype],
         M, N, K, act_group, flags, _ptr(status), _stream(stream)))
@@ -303,7 +303,7 @@ def pq2_debug_group_dots_grouped(q_planes, qsum, codes, act_group: int, stream=N
     """Exact partial dots [M][N][K/A] of the grouped GEMV's device code."""
     M, K = q_planes.shape
     N = codes.shape[0]
-    dots = torch.empty((M, N, K // act_group), dtype=torch.int32, device=q_planes.device)
+    dots = _new((M, N, K // act_group), torch.int32, q_planes.device, stream)
     _check("pq2_debug_group_dots_grouped", lib().pq2_debug_group_dots_grouped(
         _ptr(q_planes), _ptr(qsum), _ptr(codes), M, N, K, act_group, _ptr(dots), None,
         _stream(stream)))
@@ -316,8 +316,8 @@ def pq2_ptq_prepare(raw: torch.Tensor, K: int, stream=None):
     if raw.dim() != 2 or raw.stride(1) != 1 or raw.dtype != torch.uint8:
         raise ValueError("Expected a CUDA uint8 PTQ1_0 matrix")
     N = raw.shape[0]
-    qs = torch.empty((N, K // GROUP * 24), dtype=torch.uint8, device=raw.device)
-    side = torch.empty((N, K // GROUP), dtype=torch.int32, device=raw.device)
+    qs = _new((N, K // GROUP * 24), torch.uint8, raw.device, stream)
+    side = _new((N, K // GROUP), torch.int32, raw.device, stream)
     _check("pq2_ptq_prepare", lib().pq2_ptq_prepare(_ptr(raw), raw.stride(0), N, K, _ptr(qs),
                                                      _ptr(side), _stream(stream)))
     return qs, side
@@ -329,7 +329,7 @@ def pq2_ptq_mmv(q_rows, sx, qsum, qs, side, act_group: int, y=None, out_dtype=to
     M, K = q_rows.shape
     N = qs.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_rows.device)
+        y = _new((M, N), out_dtype, q_rows.device, stream)
     _check("pq2_ptq_mmv", lib().pq2_ptq_mmv(
         _ptr(q_rows), _ptr(sx), _ptr(qsum), _ptr(qs), _ptr(side), _ptr(y), _DT[y.dtype], M, N,
         K, act_group, flags, _stream(stream)))
@@ -343,9 +343,9 @@ def pq2_ptq_linear(x, qs, side, act_group: int, y=None, out_dtype=torch.float32,
     M, K = x.shape
     N = qs.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     nbytes = lib().pq2_ptq_linear_workspace_bytes(M, K, act_group)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+    ws = _new(max(nbytes, 1), torch.uint8, x.device, stream)
     _check("pq2_ptq_linear", lib().pq2_ptq_linear(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, _ptr(qs), _ptr(side), act_group, _ptr(y),
         _DT[y.dtype], _ptr(ws), ws.numel(), _stream(stream)))
@@ -356,7 +356,7 @@ def pq2_debug_ptq_dots(q_rows, qsum, qs, side, act_group: int, stream=None):
     """Exact partial dots [M][N][K/A] of the PTQ1_0 GEMV's device code."""
     M, K = q_rows.shape
     N = qs.shape[0]
-    dots = torch.empty((M, N, K // act_group), dtype=torch.int32, device=q_rows.device)
+    dots = _new((M, N, K // act_group), torch.int32, q_rows.device, stream)
     _check("pq2_debug_ptq_dots", lib().pq2_debug_ptq_dots(
         _ptr(q_rows), _ptr(qsum), _ptr(qs), _ptr(side), M, N, K, act_group, _ptr(dots),
         _stream(stream)))
@@ -370,7 +370,7 @@ def pq2_mmv_gated(q_planes, sx, qsum, codes, scales, out=None, out_dtype=torch.f
     M, K = q_planes.shape
     N = codes.shape[0]
     if out is None:
-        out = torch.empty((M, N // 2), dtype=out_dtype, device=q_planes.device)
+        out = _new((M, N // 2), out_dtype, q_planes.device, stream)
     _check("pq2_mmv_gated", lib().pq2_mmv_gated(
         _ptr(q_planes), _ptr(sx), _ptr(qsum), _ptr(codes), _ptr(scales), _ptr(out),
         _DT[out.dtype], M, N, K, flags, _ptr(status), _stream(stream)))
@@ -385,10 +385,9 @@ def pq2_linear_gated(x, codes, scales, out=None, out_dtype=torch.float32, worksp
     M, K = x.shape
     N = codes.shape[0]
     if out is None:
-        out = torch.empty((M, N // 2), dtype=out_dtype, device=x.device)
+        out = _new((M, N // 2), out_dtype, x.device, stream)
     if workspace is None:
-        workspace = torch.empty(linear_workspace_bytes(M, K), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _new(linear_workspace_bytes(M, K), torch.uint8, x.device, stream)
     _check("pq2_linear_gated", lib().pq2_linear_gated(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, _ptr(codes), _ptr(scales), _ptr(out),
         _DT[out.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -404,26 +403,26 @@ def pq2_norm_hadamard_quantize(x, w, sign, eps, residual=None, layout: int = PQ2
     if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D bf16 tensor")
     M, K = x.shape
-    q = q_buffer(M, K, layout, x.device)
-    sx = torch.empty((M, K // GROUP), dtype=torch.float32, device=x.device)
-    qsum = torch.empty((M, K // GROUP), dtype=torch.int32, device=x.device)
-    norm = torch.empty_like(x) if want_norm else None
-    rout = torch.empty_like(x) if want_residual else None
+    q = q_buffer(M, K, layout, x.device, stream)
+    sx = _new((M, K // GROUP), torch.float32, x.device, stream)
+    qsum = _new((M, K // GROUP), torch.int32, x.device, stream)
+    norm = _new(x.shape, x.dtype, x.device, stream) if want_norm else None
+    rout = _new(x.shape, x.dtype, x.device, stream) if want_residual else None
     _check("pq2_norm_hadamard_quantize", lib().pq2_norm_hadamard_quantize(
         _ptr(x), _ptr(residual), _ptr(rout), _ptr(w), _ptr(sign), float(eps), M, K,
         _ptr(norm), _ptr(q), layout, _ptr(sx), _ptr(qsum), _stream(stream)))
     return q, sx, qsum, norm, rout
 
 
-def q_buffer(M: int, K: int, layout: int, device):
+def q_buffer(M: int, K: int, layout: int, device, stream=None):
     """Output buffer of the quantiser for `layout`: fp16 [M][K] (PQ2_Q_F16,
     PQ2_Q_MMV16), uint8 [M][2K] (the two e4m3 planes of PQ2_Q_F8) or int8
     [M][K]."""
     if layout in (PQ2_Q_F16, PQ2_Q_MMV16):
-        return torch.empty((M, K), dtype=torch.float16, device=device)
+        return _new((M, K), torch.float16, device, stream)
     if layout == PQ2_Q_F8:
-        return torch.empty((M, 2 * K), dtype=torch.uint8, device=device)
-    return torch.empty((M, K), dtype=torch.int8, device=device)
+        return _new((M, 2 * K), torch.uint8, device, stream)
+    return _new((M, K), torch.int8, device, stream)
 
 
 def pq2_mm_f8(q_f8, sx, qsum, codes, scales, y=None, out_dtype=torch.float32, status=None,
@@ -432,7 +431,7 @@ def pq2_mm_f8(q_f8, sx, qsum, codes, scales, y=None, out_dtype=torch.float32, st
     M, K = q_f8.shape[0], q_f8.shape[1] // 2
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_f8.device)
+        y = _new((M, N), out_dtype, q_f8.device, stream)
     _check("pq2_mm_f8", lib().pq2_mm_f8(_ptr(q_f8), _ptr(sx), _ptr(qsum), _ptr(codes),
                                         _ptr(scales), _ptr(y), _DT[y.dtype], M, N, K,
                                         _ptr(status), _stream(stream)))
@@ -445,7 +444,7 @@ def pq2_mm(q_f16, sx, qsum, codes, scales, y=None, out_dtype=torch.float32, stat
     M, K = q_f16.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_f16.device)
+        y = _new((M, N), out_dtype, q_f16.device, stream)
     _check("pq2_mm", lib().pq2_mm(_ptr(q_f16), _ptr(sx), _ptr(qsum), _ptr(codes), _ptr(scales),
                                   _ptr(y), _DT[y.dtype], M, N, K, _ptr(status),
                                   _stream(stream)))
@@ -460,7 +459,7 @@ def pq2_debug_group_dots(q, codes, path: int, qsum=None, dots=None, status=None,
         K //= 2
     N = codes.shape[0]
     if dots is None:
-        dots = torch.empty((M, N, K // GROUP), dtype=torch.int32, device=q.device)
+        dots = _new((M, N, K // GROUP), torch.int32, q.device, stream)
     _check("pq2_debug_group_dots",
            lib().pq2_debug_group_dots(_ptr(q), _ptr(qsum), _ptr(codes), M, N, K, path,
                                       _ptr(dots), _ptr(status), _stream(stream)))
@@ -474,7 +473,7 @@ def pq2_mm_grouped(q_f16, sx, qsum, codes, scales, act_group: int, y=None,
     M, K = q_f16.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_f16.device)
+        y = _new((M, N), out_dtype, q_f16.device, stream)
     _check("pq2_mm_grouped", lib().pq2_mm_grouped(
         _ptr(q_f16), _ptr(sx), _ptr(qsum), _ptr(codes), _ptr(scales), _ptr(y), _DT[y.dtype],
         M, N, K, act_group, _ptr(status), _stream(stream)))
@@ -487,7 +486,7 @@ def pq2_mm_f8_grouped(q_f8, sx, qsum, codes, scales, act_group: int, y=None,
     M, K = q_f8.shape[0], q_f8.shape[1] // 2
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=q_f8.device)
+        y = _new((M, N), out_dtype, q_f8.device, stream)
     _check("pq2_mm_f8_grouped", lib().pq2_mm_f8_grouped(
         _ptr(q_f8), _ptr(sx), _ptr(qsum), _ptr(codes), _ptr(scales), _ptr(y), _DT[y.dtype],
         M, N, K, act_group, _ptr(status), _stream(stream)))
@@ -502,7 +501,7 @@ def pq2_debug_mm_dots_grouped(q, codes, path: int, act_group: int, dots=None, st
         K //= 2
     N = codes.shape[0]
     if dots is None:
-        dots = torch.empty((M, N, K // act_group), dtype=torch.int32, device=q.device)
+        dots = _new((M, N, K // act_group), torch.int32, q.device, stream)
     _check("pq2_debug_mm_dots_grouped", lib().pq2_debug_mm_dots_grouped(
         _ptr(q), path, _ptr(codes), M, N, K, act_group, _ptr(dots), _ptr(status),
         _stream(stream)))
@@ -522,10 +521,10 @@ def pq2_linear_grouped(x, codes, scales, act_group: int, y=None, out_dtype=torch
     M, K = x.shape
     N = codes.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     if workspace is None:
-        workspace = torch.empty(linear_grouped_workspace_bytes(M, K, act_group),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _new(linear_grouped_workspace_bytes(M, K, act_group), torch.uint8, x.device,
+                         stream)
     _check("pq2_linear_grouped", lib().pq2_linear_grouped(
         _ptr(x), _DT[x.dtype], x.stride(0), M, N, K, _ptr(codes), _ptr(scales), act_group,
         _ptr(y), _DT[y.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -563,7 +562,7 @@ def pq2_w4_prepare(codes, scales, zeros=None, group: int = 128, plane=None, stre
             raise ValueError(f"Expected contiguous {what} of shape [N][K / group]")
     nbytes = lib().pq2_w4_plane_bytes(N, K, group, int(zeros is not None))
     if plane is None:
-        plane = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=codes.device)
+        plane = _new(max(nbytes, 1), torch.uint8, codes.device, stream)
     elif plane.numel() < nbytes:
         raise Pq2Error("pq2_w4_prepare", PQ2_ERR_SHAPE)
     _check("pq2_w4_prepare", lib().pq2_w4_prepare(
@@ -596,7 +595,7 @@ def pq2_w4_mmv(x, plane, N: int, group: int = 128, zeros: bool = False, y=None,
     _check_plane(plane)
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = _new((M, N), out_dtype, x.device, stream)
     else:
         _check_out(y, (M, N))
     x_dtype, y_dtype = _dtype_of(x), _dtype_of(y)
@@ -628,10 +627,10 @@ def pq2_token_logprobs(logits, tokens=None, k: int = 0, scale: float = 1.0, entr
     T = 0 if tokens is None or not M else tokens.numel() // M
     if out is None:
         dev = logits.device
-        out = (torch.empty((M, T), dtype=torch.float32, device=dev),
-               torch.empty((M,), dtype=torch.float32, device=dev) if entropy else None,
-               torch.empty((M, k), dtype=torch.int64, device=dev),
-               torch.empty((M, k), dtype=torch.float32, device=dev))
+        out = (_new((M, T), torch.float32, dev, stream),
+               _new((M,), torch.float32, dev, stream) if entropy else None,
+               _new((M, k), torch.int64, dev, stream),
+               _new((M, k), torch.float32, dev, stream))
     else:
         _on_device(*out)
         _check_out(out[0], (M, T), torch.float32)
@@ -678,11 +677,11 @@ def pq2_norm_gate_residual(z, h, w_pre, w_post=None, gate=None, rows_per_gate: i
     if h_out is not None:
         _check_out(h_out, shape, dtype)
     elif z is not None:
-        h_out = torch.empty((M, K), dtype=dtype, device=h.device)
+        h_out = _new((M, K), dtype, h.device, stream)
     if n_out is not None:
         _check_out(n_out, shape, dtype)
     elif w_pre is not None:
-        n_out = torch.empty((M, K), dtype=dtype, device=h.device)
+        n_out = _new((M, K), dtype, h.device, stream)
     _check("pq2_norm_gate_residual", lib().pq2_norm_gate_residual(
         _ptr(z), ldz, _ptr(h), h.stride(0), code, _ptr(w_post), _ptr(gate), ldg,
         rows_per_gate, alpha, _ptr(w_pre), w_offset, eps, M, K, _ptr(h_out), _ptr(n_out),

@@ -65,3 +65,52 @@ def test_the_cache_and_the_attention(allocated, stream):
     all_on(allocated, 2, stream)
     pq2.pq2_attn_prefill(q, k, k, cu, cu, out=torch.zeros_like(q), stream=stream)
     all_on(allocated, 1, stream)
+
+
+def calls():
+    """Every other call that takes a stream, with what it allocates."""
+    def zeros(*shape, dtype=torch.uint8):
+        return torch.zeros(shape, dtype=dtype)
+    x = zeros(2, 256, dtype=torch.bfloat16)
+    codes, scales = zeros(8, 64), zeros(8, 2, dtype=torch.float16)
+    q, sx, qsum = zeros(2, 256, dtype=torch.int8), zeros(2, 2, dtype=torch.float32), zeros(2, 2)
+    q8, h = zeros(2, 512), zeros(2, 256, dtype=torch.float16)
+    w, sign = zeros(256, dtype=torch.bfloat16), zeros(256, dtype=torch.int8)
+    raw, side = zeros(8, 68), zeros(8, 2, dtype=torch.int32)
+    return [
+        (2, pq2.pq2_prepare, raw, 256), (3, pq2.pq2_quantize_act, x),
+        (3, pq2.pq2_quantize_act, x, pq2.PQ2_Q_F8), (3, pq2.pq2_quantize_act, x, pq2.PQ2_Q_F16),
+        (1, pq2.pq2_mmv, q, sx, qsum, codes, scales),
+        (1, pq2.pq2_mmv_tc, h, sx, qsum, codes, scales), (2, pq2.pq2_linear, x, codes, scales),
+        (2, pq2.linear, x, codes, scales), (3, pq2.pq2_quantize_act_grouped, x, 64),
+        (1, pq2.pq2_mmv_grouped, q, sx, qsum, codes, scales, 64),
+        (1, pq2.pq2_debug_group_dots_grouped, q, qsum, codes, 64), (2, pq2.pq2_ptq_prepare, raw, 256),
+        (1, pq2.pq2_ptq_mmv, q, sx, qsum, codes, side, 64),
+        (2, pq2.pq2_ptq_linear, x, codes, side, 64),
+        (1, pq2.pq2_debug_ptq_dots, q, qsum, codes, side, 64),
+        (1, pq2.pq2_mmv_gated, q, sx, qsum, codes, scales),
+        (2, pq2.pq2_linear_gated, x, codes, scales),
+        (5, pq2.pq2_norm_hadamard_quantize, x, w, sign, 1e-6, None, pq2.PQ2_Q_PLANES, True, True),
+        (1, pq2.pq2_mm_f8, q8, sx, qsum, codes, scales), (1, pq2.pq2_mm, h, sx, qsum, codes, scales),
+        (1, pq2.pq2_debug_group_dots, q, codes, pq2.PQ2_PATH_MMV_PLANES),
+        (1, pq2.pq2_mm_grouped, h, sx, qsum, codes, scales, 64),
+        (1, pq2.pq2_mm_f8_grouped, q8, sx, qsum, codes, scales, 64),
+        (1, pq2.pq2_debug_mm_dots_grouped, h, codes, pq2.PQ2_PATH_MM, 64),
+        (2, pq2.pq2_linear_grouped, x, codes, scales, 64),
+        (1, pq2.pq2_w4_prepare, zeros(8, 128), scales), (1, pq2.pq2_w4_mmv, x, zeros(4096), 8),
+        (4, pq2.pq2_token_logprobs, x, None, 3), (2, pq2.pq2_norm_gate_residual, x, x, w)]
+
+
+@pytest.mark.parametrize("stream", [None, Stream()])
+def test_every_other_call(allocated, stream):
+    import inspect
+    made = calls()
+    takes = {f for n, f in vars(pq2).items()
+             if inspect.isfunction(f) and not n.startswith("_") and n != "q_buffer"
+             and "stream" in inspect.signature(f).parameters}
+    assert takes == {c[1] for c in made} | {pq2.pq2_kv_store, pq2.pq2_kv_load, pq2.pq2_attn_decode,
+                                            pq2.pq2_attn_prefill}
+    for n, f, *args in made:
+        allocated.clear()
+        f(*args, stream=stream)
+        all_on(allocated, n, stream)
