@@ -245,10 +245,12 @@ def test_a_nan_costs_little():
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n,H", [(60, 2), (3000, 2), (900, 60)])
-def test_decode_of_infinities_and_nan_seen_and_not(dtype, D, n, H):
+@pytest.mark.parametrize("G", [2, 4, 6, 8, 17])
+def test_decode_of_infinities_and_nan_seen_and_not(dtype, D, n, H, G):
     """Four new tokens; the newest position's values, which only the last row sees,
-    and some that all rows see are not finite."""
-    T, G = 4, 2
+    and some that all rows see are not finite.  From one block of rows a warp to
+    several warps a slice and several items a head."""
+    T = 4
     g = A.gen(D + n)
     q = torch.randn((1, T, G * H, D), generator=g, device="cuda").to(dtype)
     k, v = (torch.randn((n, H, D), generator=g, device="cuda").to(dtype) for _ in range(2))
@@ -374,3 +376,41 @@ def test_prefill_of_many_keys_in_the_billions(dtype, D, nq, nk, order):
         # equal weights are powers of two of each other exactly; sums and out's rounding
         tol = torch.finfo(dtype).eps * size + 2.0 ** -18 * size.amax()
         assert bool(((out.double() - want[:, None]).abs() <= tol[:, None]).all())
+
+
+@pytest.mark.parametrize("cache_dtype", [BF16, F16, I8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,H", [(700, 1), (2500, 60)])
+@pytest.mark.parametrize("order", ["rising", "falling", "steps"])
+def test_decode_of_scores_in_the_billions(cache_dtype, D, n, H, order):
+    """A scale of 1e6 and products to some thousands, each exact: the output is the
+    mean of the values of the largest score, whatever their scales are."""
+    j = torch.arange(n, device="cuda")
+    p = {"rising": 500 + j // 5, "falling": 2500 - j // 5, "steps": 1000 + (j // 190) * 3}[order]
+    k = torch.zeros((n, H, D), device="cuda")
+    k[..., 0], k[..., 1] = (p // 64).float()[:, None], (p % 64).float()[:, None]
+    q = torch.zeros((1, 2 * H, D), dtype=F16 if cache_dtype == F16 else BF16, device="cuda")
+    q[..., 0], q[..., 1] = 64.0, 1.0
+    pages = -(-n // 16)
+    cache = pq2.kv_cache(pages, H, 16, D, cache_dtype)
+    v = torch.randn((n, H, D), generator=A.gen(2), device="cuda")
+    v *= 2.0 ** torch.randint(-12, 8, (n, H, 1), generator=A.gen(3), device="cuda")
+    pq2.pq2_kv_store(k, v, cache, table_of(pages, pages), ints([n]))
+    if cache_dtype == I8:  # the keys as they are, with scales of one
+        cache.k[:] = torch.cat([k, k.new_zeros(pages * 16 - n, H, D)]).to(I8) \
+            .view(pages, 16, H, D).transpose(1, 2)
+        cache.k_scales.fill_(1.0)
+    _, v = pq2.pq2_kv_load(cache, table_of(pages, pages), ints([n]), tokens=n, out_dtype=F32)
+    for m in (n, n - 1, 5 * (n // 10) + 3):
+        top = p[:m] == p[:m].max()
+        want = v[:m][top].double().mean(0).repeat_interleave(2, 0)
+        size = v[:m][top].double().abs().amax(0).repeat_interleave(2, 0)
+        # 16 bits: weights of exactly one.  8 bits: weight times scale as fp16, 2^-11
+        # of it and 2^-24 of the largest scale's; then out's rounding.
+        unit = v[:m].abs().amax(2).amax(0).double().repeat_interleave(2, 0)[:, None]
+        tol = torch.finfo(q.dtype).eps * want.abs() + 2.0 ** -18 * size + 2.0 ** -24
+        if cache_dtype == I8:
+            tol = tol + 2.0 ** -11 * size + 2.0 ** -24 * unit
+        for width in (pages, 10000):
+            out = pq2.pq2_attn_decode(q, cache, table_of(pages, width), ints([m]), scale=1e6)
+            assert bool(((out[0].double() - want).abs() <= tol).all())
