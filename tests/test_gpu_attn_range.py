@@ -60,7 +60,7 @@ def decode_and_check(q, k, v, cache_dtype, scale=1.0, wide=(False, True)):
                 unit = cache.v_scales.view(pages, H, 16)[:, h].reshape(-1)[:n].double()
                 seen = torch.arange(n, device="cuda")[None, :] < most[:, None]
                 z = torch.where(seen, rows @ kk.t() * scale, -math.inf)
-                e = torch.exp(z - z.amax(1, keepdim=True))
+                e = torch.where(seen, torch.exp(z - z.amax(1, keepdim=True)), 0.0)
                 largest = (e * unit).amax(1) + 2.0 ** -118
                 small = (2 * 127 * n * largest)[:, None]
             else:
@@ -414,3 +414,65 @@ def test_decode_of_scores_in_the_billions(cache_dtype, D, n, H, order):
         for width in (pages, 10000):
             out = pq2.pq2_attn_decode(q, cache, table_of(pages, width), ints([m]), scale=1e6)
             assert bool(((out[0].double() - want).abs() <= tol).all())
+
+
+def test_the_most_rows_of_a_key_head():
+    """64 new tokens of 256 query heads a key head, and a few."""
+    for n, T, D in ((100, 64, 64), (900, 64, 128), (40, 63, 256)):
+        q = torch.randn((1, T, 256, D), generator=A.gen(n), device="cuda").to(BF16)
+        k, v = (torch.randn((n, 1, D), generator=A.gen(n + s), device="cuda").to(BF16)
+                for s in (1, 2))
+        for cache_dtype in (BF16, I8):
+            decode_and_check(q, k.float(), v.float(), cache_dtype, scale=D ** -0.5)
+
+
+def test_the_most_sequences():
+    """65536 of one or two tokens, or none, in the decode and the prefill."""
+    B, D = 65536, 64
+    lens = torch.arange(B, device="cuda").int() * 7 % 3
+    k, v = (torch.randn((B * 2, 1, D), generator=A.gen(s), device="cuda").to(BF16) for s in (1, 2))
+    q = torch.randn((B, 2, D), generator=A.gen(3), device="cuda").to(BF16)
+    cache = pq2.kv_cache(B, 1, 16, D, BF16)
+    table = torch.randperm(B, generator=A.gen(4), device="cuda").int()[:, None]
+    two = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    pq2.pq2_kv_store(k, v, cache, table, two)
+    out = pq2.pq2_attn_decode(q, cache, table, lens)
+    kk, vv = (x.view(B, 2, D).double() for x in (k, v))
+    z = torch.einsum("bhd,bjd->bhj", q.double(), kk) * D ** -0.5
+    seen = torch.arange(2, device="cuda") < lens[:, None]
+    z = z.masked_fill(~seen[:, None], -math.inf)
+    p = torch.nan_to_num(torch.softmax(z, 2))
+    want = torch.einsum("bhj,bjd->bhd", p, vv)
+    tol = 2.0 ** -7 * torch.einsum("bhj,bjd->bhd", p, vv.abs()) + 2.0 ** -20
+    assert bool(((out.double() - want).abs() <= tol).all())
+    assert not bool(out[lens == 0].any())
+    cu_q = torch.arange(B + 1, device="cuda").int()
+    cu_k = torch.nn.functional.pad(lens.cumsum(0), (1, 0)).int()
+    at = seen.flatten()
+    out = pq2.pq2_attn_prefill(q, k[at], v[at], cu_q, cu_k)
+    assert bool(((out.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("n", [1 << 22, (1 << 24) - 5])
+def test_millions_of_keys(n):
+    """One sequence of 4 and of 16 million positions, in the prefill and the decode."""
+    D = 64
+    q = torch.randn((1, 2, D), generator=A.gen(3), device="cuda").to(BF16)
+    k, v = (torch.randn((n, 1, D), generator=A.gen(s), device="cuda", dtype=BF16) for s in (1, 2))
+    v[::2] += 1.0
+    z = torch.cat([q[0].double() @ x[:, 0].double().t() for x in k.split(1 << 20)], 1) * D ** -0.5
+    p = torch.softmax(z, 1)
+    want = sum(w @ x[:, 0].double() for w, x in zip(p.split(1 << 20, 1), v.split(1 << 20)))
+    # The sums of n weights and values of about one, in fp32 pieces: 2^-24 sqrt(n) of
+    # them each at the most likely, n 2^-24 at the very most; rounding of weights and out.
+    tol = 2.0 ** -6 * want.abs() + 2.0 ** -8
+    lse = torch.empty((1, 2), device="cuda")
+    out = pq2.pq2_attn_prefill(q, k, v, sums([1]), sums([n]), lse=lse)
+    assert bool(((out[0].double() - want).abs() <= tol).all())
+    assert float((lse[0].double() - torch.logsumexp(z, 1)).abs().max()) <= 1e-3
+    pages = -(-n // 16)
+    cache = pq2.kv_cache(pages, 1, 16, D, BF16)
+    pq2.pq2_kv_store(k, v, cache, table_of(pages, pages), ints([n]))
+    out = pq2.pq2_attn_decode(q, cache, table_of(pages, pages), ints([n]), lse=lse)
+    assert bool(((out[0].double() - want).abs() <= tol).all())
+    assert float((lse[0].double() - torch.logsumexp(z, 1)).abs().max()) <= 1e-3

@@ -73,3 +73,30 @@ def test_decode_and_load(given):
     cu = ints([0, n, n + 77])
     load = lambda s: pq2.pq2_kv_load(cache, table, lens, cu=cu, tokens=n + 77, stream=s)  # noqa: E731
     while_the_current_stream_is_busy((n + 77) * H * D * 2, load)
+
+
+def test_captured_prefills_replayed_at_once():
+    """Two graphs whose calls have workspaces (keys in parts), replayed on two streams
+    while eager calls run on a third."""
+    nq, nk, H, G, D = 60, 9000, 2, 2, 128
+    k, v = (torch.randn((nk, H, D), generator=A.gen(s), device="cuda").to(BF16) for s in (1, 2))
+    qs = [torch.randn((nq, H * G, D), generator=A.gen(s), device="cuda").to(BF16) for s in (3, 4)]
+    cu = ints([0, nq]), ints([0, nk])
+    want = [pq2.pq2_attn_prefill(q, k, v, *cu) for q in qs]
+    outs, graphs = [torch.empty_like(q) for q in qs], []
+    for q, out in zip(qs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(10):
+                pq2.pq2_attn_prefill(q, k, v, *cu, out=out)
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, s, o in zip(graphs, streams, outs):
+            with torch.cuda.stream(s):
+                o.zero_()
+                g.replay()
+        eager = [pq2.pq2_attn_prefill(q, k, v, *cu) for q in qs * 3]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+        assert all(torch.equal(o, w) for o, w in zip(eager, want * 3))
