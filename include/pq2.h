@@ -744,7 +744,10 @@ int pq2_kv_load(const pq2_kv_cache *cache, const int32_t *table,
  *            may launch two kernels), need one each.
  * Scores, the softmax and all sums are fp32.  The weights are rounded to the
  * type in which the tensor cores take them (a 16-bit cache: q's; an 8-bit one:
- * fp16), keys and values not at all.  The order of the sums follows B, T,
+ * fp16, times the value's scale and in units of the row's largest such product),
+ * keys and values not at all.  Over a 16-bit cache the sums of n weights times
+ * values are in range for values up to 2^119 / n.  A row that sees an infinity
+ * or NaN is infinite or NaN in that column.  The order of the sums follows B, T,
  * lens, table_width, the heads and the SM count; the same call gives the same bits.
  * pq2_attn_decode_workspace_bytes returns 0 for short tables and few sequences,
  * which need none, and for invalid arguments. */

@@ -27,6 +27,10 @@
 // take a part of a tile's keys each and write out, m and l in 32 bits, and a
 // second kernel joins them.
 //
+// Rows that the loop cannot do (a value that is not finite in a key tile that they
+// see in part, a maximum beyond kFar) are computed again by a warp each: 0.16 us a key
+// with 32 of them in turn, and nothing in the loop.
+//
 // Bound: the MMAs, 4 * 128 * 128 * dim operations a tile pair of 128 x 128.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -829,8 +833,8 @@ int64_t tile_pairs(int64_t B, int64_t q_rows, int64_t group, int64_t dim) {
   const int64_t per = (dim <= 128 ? 2 : 1) * (BM / group);
   return std::min(q_rows, (q_rows + per - 1) / per + B - 1);
 }
-// Parts of a tile's keys: as many as fill one wave of 152 SMs, of at least 8
-// key tiles on average, 16 at most.  64 rows of 40 heads after 16000 keys, 9
+// Parts of a tile's keys: as many as fill one wave of 152 SMs (the workspace's size is
+// asked for without a device), of at least 8 key tiles on average, 16 at most.  64 rows of 40 heads after 16000 keys, 9
 // parts: 152 -> 32 us; but 300 tile pairs in two parts: 355 -> 392 us (dim 256,
 // 16896 keys), 328 in two: 44 -> 93 us (dim 128, 2048 keys), for what the parts
 // write and read.

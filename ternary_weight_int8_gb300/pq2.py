@@ -864,8 +864,9 @@ def pq2_attn_decode(q, cache: KVCache, table, lens, scale=None, out=None, lse=No
     holds their keys and values already: q [B][heads][dim] or [B][T][heads][dim]
     -> out of q's shape.  Token t of T sees the positions before
     lens[b] - T + t + 1.  scale: 1 / sqrt(dim) if None; lse: a float32 buffer of
-    q.shape[:-1] for the rows' log-sum-exp; workspace: if None, one that is kept
-    per thread and stream (a captured call, or one with stream, gets its own)."""
+    q.shape[:-1] for the rows' log-sum-exp; workspace: if None, one of up to 11 MB
+    that is kept per thread and stream while the process lives (a captured call, or
+    one with stream, gets its own)."""
     L = lib()
     c, kv_heads, dim = _c_cache(cache)
     shape, st = q.shape, q.stride()
