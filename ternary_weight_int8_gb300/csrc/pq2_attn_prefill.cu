@@ -261,7 +261,8 @@ __device__ __noinline__ void plain_row(const T* q, const T* k, int64_t k_token, 
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (bad[e]) {
-      const uint32_t y = pack<T>(odd[e] != 0.f ? odd[e] : sum[e] / l, 0.f);
+      // l - l: NaN where a score is, whatever the values are.
+      const uint32_t y = pack<T>((odd[e] != 0.f ? odd[e] : sum[e] / l) + (l - l), 0.f);
       out[e] = *reinterpret_cast<const T*>(&y);
     }
   if (all && lse && lane == 0) *lse = m * c * kLn2 + logf(l);
@@ -833,11 +834,11 @@ int64_t tile_pairs(int64_t B, int64_t q_rows, int64_t group, int64_t dim) {
   const int64_t per = (dim <= 128 ? 2 : 1) * (BM / group);
   return std::min(q_rows, (q_rows + per - 1) / per + B - 1);
 }
-// Parts of a tile's keys: as many as fill one wave of 152 SMs (the workspace's size is
-// asked for without a device), of at least 8 key tiles on average, 16 at most.  64 rows of 40 heads after 16000 keys, 9
-// parts: 152 -> 32 us; but 300 tile pairs in two parts: 355 -> 392 us (dim 256,
-// 16896 keys), 328 in two: 44 -> 93 us (dim 128, 2048 keys), for what the parts
-// write and read.
+// Parts of a tile's keys: as many as fill one wave of 152 SMs (the workspace's size
+// is asked for without a device), of at least 8 key tiles on average, 16 at most.
+// 64 rows of 40 heads after 16000 keys, 9 parts: 152 -> 32 us; but 300 tile pairs in
+// two parts: 355 -> 392 us (dim 256, 16896 keys), 328 in two: 44 -> 93 us (dim 128,
+// 2048 keys), for what the parts write and read.
 int key_splits(int64_t B, int64_t q_rows, int64_t k_rows, int64_t q_heads, int64_t heads,
                int64_t dim) {
   const int64_t ctas = tile_pairs(B, q_rows, q_heads / heads, dim) * heads;

@@ -476,3 +476,22 @@ def test_millions_of_keys(n):
     out = pq2.pq2_attn_decode(q, cache, table_of(pages, pages), ints([n]), lse=lse)
     assert bool(((out[0].double() - want).abs() <= tol).all())
     assert float((lse[0].double() - torch.logsumexp(z, 1)).abs().max()) <= 1e-3
+
+
+@pytest.mark.parametrize("nk", [200, 9000])
+@pytest.mark.parametrize("scale", [0.1, 1e6])
+def test_a_nan_key_beside_an_infinite_value(nk, scale):
+    """Rows that see a key of NaN are NaN in every column, also where a value that they
+    see is infinite, and with scores of any size."""
+    nq = 50
+    q, k, v = (torch.randn((n, 2, 128), generator=A.gen(n), device="cuda").to(BF16)
+               for n in (nq, nk, nk + 1))
+    v = v[:nk]
+    q[..., 0], k[..., 0] = 30.0, 30.0
+    v[2, :, 7], k[nk - nq + 20] = float("inf"), float("nan")
+    lse = torch.empty((nq, 2), device="cuda")
+    out = pq2.pq2_attn_prefill(q, k, v, sums([nq]), sums([nk]), scale=scale, lse=lse)
+    assert bool(out[20:].isnan().all()) and bool(lse[20:].isnan().all())
+    assert bool((out[:20, :, 7] == float("inf")).all()) and bool(lse[:20].isfinite().all())
+    out[:20, :, 7] = 0
+    assert bool(out[:20].isfinite().all())
